@@ -91,7 +91,9 @@ typedef enum {
   CSA_OP_INDEX_TOPK = 1,
   CSA_OP_SPARSE_ATTN = 2,
   CSA_OP_HCA_ATTN = 3,
-  CSA_OP_TOPK_SELECT = 4
+  CSA_OP_TOPK_SELECT = 4,
+  CSA_OP_SPARSE_ATTN_PAGED = 5, /* n_max = table_width * page_size */
+  CSA_OP_HCA_ATTN_PAGED = 6     /* n_max = table_width * page_size */
 } csa_op_t;
 
 /* Layer constants.  Defaults of the measured model: d 512, rope_dim 64,
@@ -301,6 +303,118 @@ csa_status_t hca_attn_fp8(const csa_params_t* p, const void* q, const int32_t* q
                           const int32_t* raw_pos0, const int32_t* n_raw, int32_t raw_max,
                           const float* sink, int32_t B, int32_t Tq, void* out, void* ws,
                           size_t ws_bytes, void* stream);
+
+/* Norms of queries and keys for each head, with the position rotation in the
+ * same pass: for every head row x of token r,
+ *   y = x / sqrt(mean(x^2) + eps) * weight,
+ * then the trailing p->rope_dim dims of y are rotated by pos[r] (interleaved
+ * pairs, p's frequencies, YaRN included), both in fp32 with one rounding to
+ * the dtype.  It prepares the indexer's queries and keys, and token rows or
+ * pooled entries for a paged cache.
+ *   q  [q_rows][q_heads][dim], row r at q + r * q_stride elements (q_stride
+ *      >= q_heads * dim, q_stride * element size a multiple of 16); q_out
+ *      [q_rows][q_heads][dim] dense
+ *   k  the same with k_stride, k_heads, k_rows; row r goes to row k_slots[r]
+ *      of k_out [k_out_rows][k_heads][dim] (k_slots NULL: to row r).  A slot
+ *      of -1 skips the row; any other slot outside [0, k_out_rows) skips it
+ *      and records CSA_ERR_DEVICE_BOUNDS.  Rows of k_out that no slot names
+ *      are left untouched; two rows with one slot leave either.
+ *   q_weight, k_weight [dim] fp32 (NULL: ones); q_pos [q_rows], k_pos
+ *      [k_rows] int32 (NULL: no rotation)
+ * Either side may have 0 rows (its pointers may then be NULL).  dim is a
+ * multiple of 8 in [8, 1024], at least rope_dim; eps > 0; p->d is not used.
+ * q_out may be q itself when q_stride = q_heads * dim (likewise k without
+ * slots); other overlaps of inputs and outputs are not allowed.  The mean of
+ * squares is fp32: rows must stay below 2^63 / sqrt(dim) in magnitude. */
+csa_status_t csa_norm_rope(const csa_params_t* p, csa_dtype_t dtype, int32_t dim, float eps,
+                           const void* q, int64_t q_stride, int32_t q_heads, int32_t q_rows,
+                           const float* q_weight, const int32_t* q_pos, void* q_out, const void* k,
+                           int64_t k_stride, int32_t k_heads, int32_t k_rows,
+                           const float* k_weight, const int32_t* k_pos, const int32_t* k_slots,
+                           int32_t k_out_rows, void* k_out, void* stream);
+
+/* Microscaled 4-bit floating point (OCP Microscaling Formats v1.0, MXFP4):
+ * blocks of 32 values along a row share one E8M0 scale.
+ *   rows   [n][d] (bf16 or fp32), row i at rows + i * row_stride elements
+ *          (row_stride >= d, row_stride * element size a multiple of 16),
+ *          d a multiple of 32 in [32, 1024]
+ *   slots  [n] int32 (NULL: row i goes to row i): the row of codes and scales
+ *          that row i is written to; -1 skips it, any other slot outside
+ *          [0, out_rows) skips it and records CSA_ERR_DEVICE_BOUNDS
+ *   codes  [out_rows][d / 2] uint8: E2M1 codes (values 0, 0.5, 1, 1.5, 2, 3,
+ *          4, 6; bit 3 the sign), the even dim in the low four bits: x / scale
+ *          to the nearest, ties to the even code, past 6 to 6
+ *   scales [out_rows][d / 32] uint8, E8M0: byte e stands for 2^(e - 127);
+ *          2^(floor(log2 max|block|) - 2), not below 2^-127, 1 for a block of
+ *          zeros; 255 (NaN, codes 0) for a block that holds an infinity or NaN
+ *   values [n][d] (nullable, the rows' dtype): the values that the codes
+ *          stand for (exact), row i at row i, skipped rows included
+ * Rows of codes and scales that no slot names are left untouched. */
+csa_status_t csa_quantize_mxfp4(csa_dtype_t dtype, const void* rows, int64_t row_stride, int64_t n,
+                                int32_t d, const int32_t* slots, int64_t out_rows, uint8_t* codes,
+                                uint8_t* scales, void* values, void* stream);
+
+/* Paged caches (the calls below).  A pool of n_pages pages of page_size rows
+ * (a power of two in [8, 2^20]); sequence b's entry j is row j % page_size of
+ * page page_table[b][j / page_size], page_table [B][table_width] int32.  Only
+ * the table entries of pages that hold a needed entry are read, and only the
+ * needed rows count: the rest of a page may hold anything.  A table entry
+ * outside [0, n_pages) records CSA_ERR_DEVICE_BOUNDS and its rows are
+ * skipped.  Pages may be shared between sequences. */
+
+/* Step 2a on MXFP4 queries and paged MXFP4 keys: csa_index_scores with
+ *   q_codes [B][Tq][H_I][d_I / 2], q_scales [B][Tq][H_I][d_I / 32]
+ *   k_codes [n_pages][page_size][d_I / 2], k_scales [n_pages][page_size]
+ *           [d_I / 32], page_table [B][table_width]; or, with page_table NULL
+ *           and table_width 0, contiguous keys [B][n_max][...]
+ *   scores  [B][Tq][n_max] fp32, n_max <= table_width * page_size; entries j
+ *           >= n_visible, and entries of pages outside the pool, are not
+ *           written
+ * Products are exact, sums fp32.  d_I a multiple of 32.  A NaN in a query
+ * or key (scale byte 255) gives NaN scores. */
+csa_status_t csa_index_scores_mxfp4(const csa_params_t* p, const uint8_t* q_codes,
+                                    const uint8_t* q_scales, const float* w,
+                                    const uint8_t* k_codes, const uint8_t* k_scales,
+                                    const int32_t* page_table, int32_t table_width,
+                                    int32_t n_pages, int32_t page_size, const int32_t* q_pos,
+                                    const int32_t* n_cmp, int32_t B, int32_t Tq, int32_t n_max,
+                                    float* scores, void* stream);
+
+/* The same with csa_topk_select in one call (scores kept in `ws` of
+ * csa_workspace_size(CSA_OP_INDEX_TOPK, B, Tq, n_max) bytes).  The selection
+ * is unspecified for queries with an entry in a page outside the pool. */
+csa_status_t csa_index_topk_mxfp4(const csa_params_t* p, const uint8_t* q_codes,
+                                  const uint8_t* q_scales, const float* w, const uint8_t* k_codes,
+                                  const uint8_t* k_scales, const int32_t* page_table,
+                                  int32_t table_width, int32_t n_pages, int32_t page_size,
+                                  const int32_t* q_pos, const int32_t* n_cmp, int32_t B, int32_t Tq,
+                                  int32_t n_max, int32_t* idx_out, void* ws, size_t ws_bytes,
+                                  void* stream);
+
+/* Step 3 over a paged entry cache: csa_sparse_attn with kv_pages [n_pages]
+ * [page_size][d] and page_table in place of kv_cmp; idx holds entry numbers
+ * of the sequence (-1 = unused, >= table_width * page_size: skipped and
+ * recorded).  The window's raw rows stay contiguous per sequence.
+ * ws: csa_workspace_size(CSA_OP_SPARSE_ATTN_PAGED). */
+csa_status_t csa_sparse_attn_paged(const csa_params_t* p, csa_dtype_t dtype, const void* q,
+                                   const int32_t* q_pos, const void* kv_pages, int32_t n_pages,
+                                   int32_t page_size, const int32_t* page_table,
+                                   int32_t table_width, const int32_t* idx, const void* kv_raw,
+                                   const int32_t* raw_pos0, const int32_t* n_raw, int32_t raw_max,
+                                   const float* sink, int32_t B, int32_t Tq, void* out, void* ws,
+                                   size_t ws_bytes, void* stream);
+
+/* Step 4 over a paged entry cache of any length: hca_attn with kv_pages and
+ * page_table in place of kv_cmp.  With width = stride = 1 every token is its
+ * own entry: attention of new tokens over a paged cache of one shared KV row
+ * per token.  The rows are split over the GPU and joined.
+ * ws: csa_workspace_size(CSA_OP_HCA_ATTN_PAGED). */
+csa_status_t hca_attn_paged(const csa_params_t* p, csa_dtype_t dtype, const void* q,
+                            const int32_t* q_pos, const void* kv_pages, int32_t n_pages,
+                            int32_t page_size, const int32_t* page_table, int32_t table_width,
+                            const int32_t* n_cmp, const void* kv_raw, const int32_t* raw_pos0,
+                            const int32_t* n_raw, int32_t raw_max, const float* sink, int32_t B,
+                            int32_t Tq, void* out, void* ws, size_t ws_bytes, void* stream);
 
 /* Indexer + top-k that allocates nothing: the same computation and
  * arguments as csa_index_topk, without `ws`.  The pages have no counterpart

@@ -18,6 +18,7 @@ LIB_PATH = os.path.join(_HERE, "libcsa.so")
 
 CSA_F32, CSA_BF16 = 0, 1
 CSA_OP_COMPRESS, CSA_OP_INDEX_TOPK, CSA_OP_SPARSE_ATTN, CSA_OP_HCA_ATTN, CSA_OP_TOPK_SELECT = range(5)
+CSA_OP_SPARSE_ATTN_PAGED, CSA_OP_HCA_ATTN_PAGED = 5, 6
 
 STATUS = {
     0: "CSA_OK", 1: "CSA_ERR_INVALID_ARGUMENT", 2: "CSA_ERR_MISALIGNED",
@@ -115,6 +116,17 @@ def _load():
     lib.hca_attn_fp8.argtypes = list(lib.csa_sparse_attn_fp8.argtypes)
     lib.csa_index_topk_noalloc.argtypes = [_PP, ctypes.c_int, _P, _P, _P, _P, _P, _I, _I, _I, _P,
                                            _P]
+    _L, _Z = ctypes.c_int64, ctypes.c_size_t
+    lib.csa_norm_rope.argtypes = [_PP, ctypes.c_int, _I, ctypes.c_float, _P, _L, _I, _I, _P, _P, _P,
+                                  _P, _L, _I, _I, _P, _P, _P, _I, _P, _P]
+    lib.csa_quantize_mxfp4.argtypes = [ctypes.c_int, _P, _L, _L, _I, _P, _L, _P, _P, _P, _P]
+    lib.csa_index_scores_mxfp4.argtypes = [_PP, _P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _I, _I,
+                                           _I, _P, _P]
+    lib.csa_index_topk_mxfp4.argtypes = [_PP, _P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _I, _I, _I,
+                                         _P, _P, _Z, _P]
+    lib.csa_sparse_attn_paged.argtypes = [_PP, ctypes.c_int, _P, _P, _P, _I, _I, _P, _I, _P, _P, _P,
+                                          _P, _I, _P, _I, _I, _P, _P, _Z, _P]
+    lib.hca_attn_paged.argtypes = list(lib.csa_sparse_attn_paged.argtypes)
     lib.csa_poll_device_error.argtypes = [_P]
     lib.csa_launch_count.restype = ctypes.c_uint64
     lib.csa_launch_count.argtypes = []
@@ -125,7 +137,8 @@ def _load():
     for f in ("csa_workspace_size", "csa_compress", "csa_index_scores", "csa_topk_select",
               "csa_index_topk", "csa_sparse_attn", "hca_attn", "csa_poll_device_error",
               "csa_compress_append", "csa_quantize_fp8", "csa_sparse_attn_fp8", "hca_attn_fp8",
-              "csa_reuse_attn",
+              "csa_reuse_attn", "csa_norm_rope", "csa_quantize_mxfp4", "csa_index_scores_mxfp4",
+              "csa_index_topk_mxfp4", "csa_sparse_attn_paged", "hca_attn_paged",
               "csa_index_topk_noalloc"):
         getattr(lib, f).restype = ctypes.c_int
     _lib = lib
@@ -428,3 +441,239 @@ def hca_attn_fp8(p: Params, q, q_pos, kv_cmp, cmp_scale, n_cmp, kv_raw, raw_scal
     _req(n_cmp, "n_cmp", torch.int32, 1)
     _attn_fp8(_load().hca_attn_fp8, p, q, q_pos, kv_cmp, cmp_scale, n_cmp, kv_raw, raw_scale,
               raw_pos0, n_raw, sink, out, ws, stream)
+
+
+# ---------------------------------------------------------------------------
+# The paged, 4-bit serving path.  These calls also check that every tensor is
+# on the current device and that the shapes agree.
+
+def _arg(t, name, dtype, shape, dev):
+    """A contiguous tensor of this dtype and shape (None: any size) on `dev`."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    have = t.shape
+    if len(have) != len(shape) or any(w is not None and w != h for h, w in zip(have, shape)):
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(have)}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _device_of(t, name):
+    """The tensor's device, which has to be the current one (the library
+    launches on the current device)."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    dev = t.device
+    if dev.index != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on {dev}, the current device is "
+                         f"cuda:{torch._C._cuda_getDevice()}")
+    return dev
+
+
+def _ws_arg(ws, dev):
+    """(pointer, bytes) of a workspace tensor or None."""
+    if ws is None:
+        return None, 0
+    if ws.device != dev:
+        raise ValueError(f"ws is on {ws.device}, expected {dev}")
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _head_rows(t, name, dtype, dim, dev):
+    """Rows [rows][heads][dim] whose heads are dense, at any row stride."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[2] != dim:
+        raise ValueError(f"{name} must have shape [rows, heads, {dim}], got {list(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    rows, heads, _ = t.shape
+    sr, sh, sd = t.stride()
+    if sd != 1 or (heads > 1 and sh != dim):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return t.data_ptr(), (sr if rows > 1 else heads * dim), heads, rows
+
+
+def csa_norm_rope(p: Params, eps: float, q=None, q_weight=None, q_pos=None, q_out=None, k=None,
+                  k_weight=None, k_pos=None, k_out=None, k_slots=None, stream=None):
+    """RMS norm (fp32 weights [dim], None: ones) of every head of q
+    [rows][heads][dim] and k [k_rows][k_heads][dim] and rotation of their
+    trailing p.rope_dim dims by q_pos / k_pos (None: none) in one pass.  The
+    rows of q and k may be strided (slices of one projection).  q_out as q,
+    dense; row r of k goes to row k_slots[r] (-1: skipped; None: r) of k_out
+    [n][k_heads][dim].  Either side may be None."""
+    import torch
+    first, name = (q, "q") if q is not None else (k, "k")
+    dev = _device_of(first, name)
+    dt = first.dtype
+    code = _dtype_code(first)
+    if first.dim() != 3:
+        raise ValueError(f"{name} must have 3 dims, got {list(first.shape)}")
+    dim = first.shape[2]
+    f32, i32 = torch.float32, torch.int32
+    qa = ka = (None, 0, 1, 0, None, None, None)
+    if q is not None:
+        ptr, st, heads, rows = _head_rows(q, "q", dt, dim, dev)
+        qa = (ptr, st, heads, rows,
+              None if q_weight is None else _arg(q_weight, "q_weight", f32, (dim,), dev),
+              None if q_pos is None else _arg(q_pos, "q_pos", i32, (rows,), dev),
+              _arg(q_out, "q_out", dt, (rows, heads, dim), dev))
+    n_out, slots = 0, None
+    if k is not None:
+        ptr, st, heads, rows = _head_rows(k, "k", dt, dim, dev)
+        out = _arg(k_out, "k_out", dt, (rows if k_slots is None else None, heads, dim), dev)
+        n_out = k_out.shape[0]
+        slots = None if k_slots is None else _arg(k_slots, "k_slots", i32, (rows,), dev)
+        ka = (ptr, st, heads, rows,
+              None if k_weight is None else _arg(k_weight, "k_weight", f32, (dim,), dev),
+              None if k_pos is None else _arg(k_pos, "k_pos", i32, (rows,), dev), out)
+    _check(_load().csa_norm_rope(ctypes.byref(p.c()), code, dim, eps, *qa, *ka[:6], slots, n_out,
+                                 ka[6], _stream(stream)))
+
+
+def csa_quantize_mxfp4(rows, codes, scales, slots=None, values=None, stream=None):
+    """Rows [..., d] (bf16 or fp32; a 2-D tensor may have strided rows) ->
+    MXFP4 codes [n_out, ..., d / 2] and E8M0 scales [n_out, ..., d / 32]
+    uint8.  With slots [n] int32, row i of the 2-D rows goes to row slots[i] of
+    the 2-D (or paged [pages][page][...]) codes and scales (-1: skipped).
+    values (rows' shape and dtype) receives the values the codes stand for."""
+    import torch
+    dev = _device_of(rows, "rows")
+    code = _dtype_code(rows)
+    if rows.dim() < 1:
+        raise ValueError("rows must have at least 1 dim")
+    d = rows.shape[-1]
+    n = rows.numel() // d if d else 0
+    if rows.is_contiguous():
+        stride = d
+    elif rows.dim() == 2 and rows.stride(1) == 1:
+        stride = rows.stride(0)
+    else:
+        raise ValueError("rows must be contiguous, or 2-D with contiguous rows")
+    for t, name, div in ((codes, "codes", 2), (scales, "scales", 32)):
+        _arg(t, name, torch.uint8, (None,) * (t.dim() - 1) + (d // div,), dev)
+    n_out = codes.numel() // (d // 2) if d >= 2 else 0
+    if tuple(codes.shape[:-1]) != tuple(scales.shape[:-1]):
+        raise ValueError("codes and scales must have the same rows")
+    sp = None
+    if slots is not None:
+        if rows.dim() != 2:
+            raise ValueError("slots need 2-D rows")
+        sp = _arg(slots, "slots", torch.int32, (n,), dev)
+    elif tuple(codes.shape[:-1]) != tuple(rows.shape[:-1]):
+        raise ValueError("without slots, codes and scales must have the rows' leading dims")
+    vp = None if values is None else _arg(values, "values", rows.dtype, tuple(rows.shape), dev)
+    _check(_load().csa_quantize_mxfp4(code, rows.data_ptr(), stride, n, d, sp, n_out,
+                                      codes.data_ptr(), scales.data_ptr(), vp, _stream(stream)))
+
+
+def _mx_index_args(p, q_codes, q_scales, w, k_codes, k_scales, page_table, q_pos, n_cmp, n_max):
+    """Checked arguments of the two indexer calls, in the C order from
+    q_codes to n_max."""
+    import torch
+    dev = _device_of(q_codes, "q_codes")
+    u8, i32 = torch.uint8, torch.int32
+    H, D = p.idx_heads, p.idx_dim
+    if not isinstance(q_pos, torch.Tensor) or q_pos.dim() != 2:
+        raise ValueError("q_pos must be a [B, Tq] tensor")
+    B, Tq = q_pos.shape
+    qc = _arg(q_codes, "q_codes", u8, (B, Tq, H, D // 2), dev)
+    qs = _arg(q_scales, "q_scales", u8, (B, Tq, H, D // 32), dev)
+    wp = _arg(w, "w", torch.float32, (B, Tq, H), dev)
+    kc = _arg(k_codes, "k_codes", u8, (None, None, D // 2), dev)
+    pages, page = k_codes.shape[0], k_codes.shape[1]
+    ks = _arg(k_scales, "k_scales", u8, (pages, page, D // 32), dev)
+    if page_table is None:
+        if pages != B or (n_max is not None and page != n_max):
+            raise ValueError(f"contiguous keys must be [B, n_max, ...], got {list(k_codes.shape)}")
+        tp, width, n_max = None, 0, page
+    else:
+        tp = _arg(page_table, "page_table", i32, (B, None), dev)
+        width = page_table.shape[1]
+        n_max = width * page if n_max is None else n_max
+    return dev, (qc, qs, wp, kc, ks, tp, width, pages, page,
+                 _arg(q_pos, "q_pos", i32, (B, Tq), dev), _arg(n_cmp, "n_cmp", i32, (B,), dev), B,
+                 Tq, n_max)
+
+
+def csa_index_scores_mxfp4(p: Params, q_codes, q_scales, w, k_codes, k_scales, page_table, q_pos,
+                           n_cmp, scores, stream=None):
+    """Indexer scores on MXFP4 queries [B][Tq][H_I][d_I/2] and keys
+    [n_pages][page][d_I/2] found through page_table [B][width] (None: keys
+    [B][n_max][d_I/2]) -> scores [B][Tq][n_max] of the visible entries."""
+    import torch
+    if not isinstance(scores, torch.Tensor) or scores.dim() != 3:
+        raise ValueError("scores must be a [B, Tq, n_max] tensor")
+    dev, a = _mx_index_args(p, q_codes, q_scales, w, k_codes, k_scales, page_table, q_pos, n_cmp,
+                            scores.shape[2])
+    sp = _arg(scores, "scores", torch.float32, (a[11], a[12], a[13]), dev)
+    _check(_load().csa_index_scores_mxfp4(ctypes.byref(p.c()), *a, sp, _stream(stream)))
+
+
+def csa_index_topk_mxfp4(p: Params, q_codes, q_scales, w, k_codes, k_scales, page_table, q_pos,
+                         n_cmp, idx_out, ws, n_max=None, stream=None):
+    """csa_index_scores_mxfp4 + top-k; n_max: entries scored at most (None:
+    all the table holds); ws: csa_workspace_size(CSA_OP_INDEX_TOPK, B, Tq,
+    n_max) bytes."""
+    import torch
+    dev, a = _mx_index_args(p, q_codes, q_scales, w, k_codes, k_scales, page_table, q_pos, n_cmp,
+                            n_max)
+    ip = _arg(idx_out, "idx_out", torch.int32, (a[11], a[12], p.topk), dev)
+    wp, nb = _ws_arg(ws, dev)
+    _check(_load().csa_index_topk_mxfp4(ctypes.byref(p.c()), *a, ip, wp, nb, _stream(stream)))
+
+
+def _attn_paged(fn, p, q, q_pos, kv_pages, page_table, sel, sel_name, sel_shape, kv_raw, raw_pos0,
+                n_raw, sink, out, ws, stream):
+    import torch
+    dev = _device_of(q, "q")
+    code = _dtype_code(q)
+    dt, i32 = q.dtype, torch.int32
+    if not isinstance(q_pos, torch.Tensor) or q_pos.dim() != 2:
+        raise ValueError("q_pos must be a [B, Tq] tensor")
+    B, Tq = q_pos.shape
+    H, d = p.n_heads, p.d
+    qp = _arg(q, "q", dt, (B, Tq, H, d), dev)
+    pp = _arg(q_pos, "q_pos", i32, (B, Tq), dev)
+    kp = _arg(kv_pages, "kv_pages", dt, (None, None, d), dev)
+    tp = _arg(page_table, "page_table", i32, (B, None), dev)
+    sp = _arg(sel, sel_name, i32, (B, Tq, p.topk) if sel_shape else (B,), dev)
+    rp = _arg(kv_raw, "kv_raw", dt, (B, None, d), dev)
+    r0 = _arg(raw_pos0, "raw_pos0", i32, (B,), dev)
+    nr = _arg(n_raw, "n_raw", i32, (B,), dev)
+    kp_s = _arg(sink, "sink", torch.float32, (H,), dev)
+    op = _arg(out, "out", dt, (B, Tq, H, d), dev)
+    wp, nb = _ws_arg(ws, dev)
+    _check(fn(ctypes.byref(p.c()), code, qp, pp, kp, kv_pages.shape[0], kv_pages.shape[1], tp,
+              page_table.shape[1], sp, rp, r0, nr, kv_raw.shape[1], kp_s, B, Tq, op, wp, nb,
+              _stream(stream)))
+
+
+def csa_sparse_attn_paged(p: Params, q, q_pos, kv_pages, page_table, idx, kv_raw, raw_pos0, n_raw,
+                          sink, out, ws=None, stream=None):
+    """csa_sparse_attn over entries in pages: kv_pages [n_pages][page][d],
+    page_table [B][width] int32, idx [B][Tq][topk] entry numbers."""
+    _attn_paged(_load().csa_sparse_attn_paged, p, q, q_pos, kv_pages, page_table, idx, "idx", True,
+                kv_raw, raw_pos0, n_raw, sink, out, ws, stream)
+
+
+def hca_attn_paged(p: Params, q, q_pos, kv_pages, page_table, n_cmp, kv_raw, raw_pos0, n_raw, sink,
+                   out, ws=None, stream=None):
+    """hca_attn over entries in pages, at any cache length: kv_pages
+    [n_pages][page][d], page_table [B][width] int32, n_cmp [B]."""
+    _attn_paged(_load().hca_attn_paged, p, q, q_pos, kv_pages, page_table, n_cmp, "n_cmp", False,
+                kv_raw, raw_pos0, n_raw, sink, out, ws, stream)

@@ -13,6 +13,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "attn_paged_simt.cuh"
 #include "attn_pair.cuh"
 #include "attn_simt.cuh"
 #include "common.cuh"
@@ -21,6 +22,8 @@
 #include "csa.h"
 #include "indexer_simt.cuh"
 #include "indexer_tc.cuh"
+#include "mxfp4.cuh"
+#include "norm_rope.cuh"
 #include "topk.cuh"
 #include "topk_block.cuh"
 
@@ -426,6 +429,28 @@ size_t attn_ws_bytes(const csa_params_t* p, csa_dtype_t dtype, bool hca, int B, 
          round_up(units * 2 * kApHeads * sizeof(float), 256);
 }
 
+// Splits of the generic paged attention: enough CTAs (one per token, group
+// of heads and split) for about four per SM, at least 32 rows a split.
+int paged_simt_heads(const csa_params_t* p) {  // heads per CTA: 64 registers of q and sums
+  return p->d <= 128 ? 8 : (p->d == 256 ? 4 : (p->d == 512 ? 2 : 1));
+}
+
+int paged_simt_splits(const csa_params_t* p, bool hca, int B, int Tq, int n_max) {
+  const long long hg = paged_simt_heads(p);
+  const long long ctas = (long long)B * Tq * ((p->n_heads + hg - 1) / hg);
+  const long long rows = (long long)(hca ? n_max : p->topk) + p->window;
+  long long s = 4LL * num_sms() / ctas;
+  if (s > rows / 32) s = rows / 32;
+  if (s > 64) s = 64;
+  return s < 1 ? 1 : (int)s;
+}
+
+size_t paged_simt_ws_bytes(const csa_params_t* p, bool hca, int B, int Tq, int n_max) {
+  const int sp = paged_simt_splits(p, hca, B, Tq, n_max);
+  if (sp == 1) return 0;
+  return round_up((size_t)B * Tq * p->n_heads * sp * (p->d + 2) * sizeof(float), 256);
+}
+
 // Limit of every bounded device-side wait (csa_set_wait_limit_ns).
 constexpr unsigned long long kDefaultWaitNs = 2000000000ull;
 std::atomic<unsigned long long> g_wait_ns{kDefaultWaitNs};
@@ -478,6 +503,12 @@ CSA_API csa_status_t csa_workspace_size(const csa_params_t* p, csa_op_t op, int3
       return CSA_OK;
     case CSA_OP_SPARSE_ATTN: *bytes = attn_ws_bytes(p, CSA_BF16, false, B, Tq, n_max); return CSA_OK;
     case CSA_OP_HCA_ATTN: *bytes = attn_ws_bytes(p, CSA_BF16, true, B, Tq, n_max); return CSA_OK;
+    case CSA_OP_SPARSE_ATTN_PAGED:
+      *bytes = paged_simt_ws_bytes(p, false, B, Tq, n_max);
+      return CSA_OK;
+    case CSA_OP_HCA_ATTN_PAGED:
+      *bytes = paged_simt_ws_bytes(p, true, B, Tq, n_max);
+      return CSA_OK;
   }
   return fail(CSA_ERR_INVALID_ARGUMENT, "bad op %d", (int)op);
 }
@@ -1073,6 +1104,386 @@ CSA_API csa_status_t hca_attn_fp8(const csa_params_t* p, const void* q, const in
   a.cmp_scale = cmp_scale;
   a.raw_scale = raw_scale;
   return launch_attn_tc<true, true>(p, a, ws, ws_bytes, (cudaStream_t)stream);
+}
+
+// ---------------------------------------------------------------------------
+// The paged, 4-bit serving path: norm + RoPE of query and key heads, MXFP4
+// rows, the indexer's product on them, attention over paged caches.
+// ---------------------------------------------------------------------------
+template <typename T, int NV>
+static cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t s) {
+  return launch_ex(k_norm_rope<T, NV>, dim3((unsigned)(a.side[0].blocks + a.side[1].blocks)),
+                   dim3(kNormThreads), 0, s, 1, a);
+}
+
+static csa_status_t norm_side(NormSide& sd, const char* name, csa_dtype_t dtype, const void* x,
+                              int64_t row_stride, int32_t heads, int32_t rows, const float* weight,
+                              const int32_t* pos, const int32_t* slots, int32_t out_rows, void* out,
+                              int32_t dim) {
+  const int esz = dtype == CSA_BF16 ? 2 : 4;
+  if (rows < 0 || out_rows < 0 || heads < 1 || heads > 65535)
+    return fail(CSA_ERR_UNSUPPORTED_SHAPE, "%s: rows=%d heads=%d out rows=%d", name, rows, heads,
+                out_rows);
+  if (rows == 0) return CSA_OK;
+  CSA_CHECK(check_ptr(x, name));
+  CSA_CHECK(check_ptr(weight, "weight", true));
+  CSA_CHECK(check_ptr(pos, "pos", true));
+  CSA_CHECK(check_ptr(slots, "slots", true));
+  CSA_CHECK(check_ptr(out, "out", out_rows == 0));
+  if (row_stride < (int64_t)heads * dim)
+    return fail(CSA_ERR_INVALID_ARGUMENT, "%s: row stride %lld below heads * dim = %lld", name,
+                (long long)row_stride, (long long)heads * dim);
+  if ((row_stride * esz) & 15)
+    return fail(CSA_ERR_MISALIGNED, "%s: rows are not 16-byte aligned", name);
+  if (slots == nullptr && out_rows < rows)
+    return fail(CSA_ERR_INVALID_ARGUMENT, "%s: %d output rows for %d rows", name, out_rows, rows);
+  sd.x = x;
+  sd.row_stride = row_stride;
+  sd.weight = weight;
+  sd.pos = pos;
+  sd.slots = slots;
+  sd.out = out;
+  sd.rows = rows;
+  sd.heads = heads;
+  sd.out_rows = out_rows;
+  return CSA_OK;
+}
+
+CSA_API csa_status_t csa_norm_rope(const csa_params_t* p, csa_dtype_t dtype, int32_t dim, float eps,
+                                   const void* q, int64_t q_stride, int32_t q_heads, int32_t q_rows,
+                                   const float* q_weight, const int32_t* q_pos, void* q_out,
+                                   const void* k, int64_t k_stride, int32_t k_heads, int32_t k_rows,
+                                   const float* k_weight, const int32_t* k_pos,
+                                   const int32_t* k_slots, int32_t k_out_rows, void* k_out,
+                                   void* stream) {
+  const CallRange trace("csa_norm_rope");
+  CSA_CHECK(check_params(p));
+  CSA_CHECK(check_dtype(dtype));
+  if (dim < 8 || dim > 1024 || (dim & 7) || p->rope_dim > dim)
+    return fail(CSA_ERR_UNSUPPORTED_SHAPE, "dim=%d: a multiple of 8 in [8, 1024], >= rope_dim=%d",
+                dim, p->rope_dim);
+  if (!(eps > 0.f) || !std::isfinite(eps))
+    return fail(CSA_ERR_INVALID_ARGUMENT, "eps must be positive and finite");
+  NormRopeArgs a{};
+  CSA_CHECK(norm_side(a.side[0], "q", dtype, q, q_stride, q_heads, q_rows, q_weight, q_pos, nullptr,
+                      q_rows, q_out, dim));
+  CSA_CHECK(norm_side(a.side[1], "k", dtype, k, k_stride, k_heads, k_rows, k_weight, k_pos, k_slots,
+                      k_out_rows, k_out, dim));
+  if (q_rows == 0 && k_rows == 0) return CSA_OK;
+  CSA_CHECK(check_device());
+  const int vec = dtype == CSA_BF16 ? 8 : 4;
+  const int vecs = dim / vec;
+  a.dim = dim;
+  a.rope_dim = p->rope_dim;
+  a.eps = eps;
+  a.group = 1;
+  while (a.group < vecs && a.group < 32) a.group *= 2;
+  const int nv = vecs <= 32 ? 1 : (vecs <= 64 ? 2 : (vecs <= 128 ? 4 : 8));
+  const long long gpc = kNormThreads / a.group;  // groups per CTA
+  long long total = 0;
+  for (NormSide& sd : a.side) {
+    if (sd.rows == 0) {
+      sd.hgroups = sd.hpg = 1;
+      continue;
+    }
+    // heads per group: one while the rows are few (every row its own lanes),
+    // more when there is enough work to fill the GPU several times over
+    sd.hpg = 1;
+    const long long work = (long long)sd.rows * sd.heads;
+    while (sd.hpg < 8 && 2 * sd.hpg <= sd.heads && work / (2 * sd.hpg) >= 16LL * num_sms() * gpc)
+      sd.hpg *= 2;
+    sd.hgroups = (sd.heads + sd.hpg - 1) / sd.hpg;
+    const long long blocks = ((long long)sd.rows * sd.hgroups + gpc - 1) / gpc;
+    total += blocks;
+    if (total > 2147483647LL) return fail(CSA_ERR_UNSUPPORTED_SHAPE, "too many rows");
+    sd.blocks = (int)blocks;
+  }
+  const RopeSpec rope = rope_spec(p);
+  for (int i = 0; i < a.rope_dim / 2; ++i) a.freq[i] = rope_freq(rope, i);
+  cudaStream_t s = (cudaStream_t)stream;
+  cudaError_t e;
+  if (dtype == CSA_BF16)
+    e = nv == 1 ? launch_norm_rope<__nv_bfloat16, 1>(a, s)
+                : (nv == 2 ? launch_norm_rope<__nv_bfloat16, 2>(a, s)
+                           : launch_norm_rope<__nv_bfloat16, 4>(a, s));
+  else
+    e = nv == 1   ? launch_norm_rope<float, 1>(a, s)
+        : nv == 2 ? launch_norm_rope<float, 2>(a, s)
+        : nv == 4 ? launch_norm_rope<float, 4>(a, s)
+                  : launch_norm_rope<float, 8>(a, s);
+  if (e != cudaSuccess) return cuda_fail(e, "k_norm_rope");
+  return launched("k_norm_rope");
+}
+
+CSA_API csa_status_t csa_quantize_mxfp4(csa_dtype_t dtype, const void* rows, int64_t row_stride,
+                                        int64_t n, int32_t d, const int32_t* slots,
+                                        int64_t out_rows, uint8_t* codes, uint8_t* scales,
+                                        void* values, void* stream) {
+  const CallRange trace("csa_quantize_mxfp4");
+  CSA_CHECK(check_dtype(dtype));
+  if (n < 0 || out_rows < 0 || d < 32 || d > 1024 || (d & 31))
+    return fail(CSA_ERR_UNSUPPORTED_SHAPE, "n=%lld out rows=%lld d=%d: d a multiple of 32 in [32, 1024]",
+                (long long)n, (long long)out_rows, d);
+  if (n == 0) return CSA_OK;
+  const int esz = dtype == CSA_BF16 ? 2 : 4;
+  CSA_CHECK(check_ptr(rows, "rows"));
+  CSA_CHECK(check_ptr(slots, "slots", true));
+  CSA_CHECK(check_ptr(codes, "codes", out_rows == 0));
+  CSA_CHECK(check_ptr(scales, "scales", out_rows == 0));
+  CSA_CHECK(check_ptr(values, "values", true));
+  if (row_stride < d) return fail(CSA_ERR_INVALID_ARGUMENT, "row stride %lld below d=%d", (long long)row_stride, d);
+  if ((row_stride * esz) & 15) return fail(CSA_ERR_MISALIGNED, "rows are not 16-byte aligned");
+  if (slots == nullptr && out_rows < n)
+    return fail(CSA_ERR_INVALID_ARGUMENT, "%lld output rows for %lld rows", (long long)out_rows,
+                (long long)n);
+  CSA_CHECK(check_device());
+  cudaStream_t s = (cudaStream_t)stream;
+  const unsigned cpr = (unsigned)d / 8;
+  // chunks of 8 values are counted in 32 bits: at most 2^30 of them a launch
+  const long long per = (1LL << 30) / cpr;
+  for (long long i0 = 0; i0 < n; i0 += per) {
+    const unsigned m = (unsigned)std::min<long long>(per, n - i0);
+    const unsigned ctas = (unsigned)(((long long)m * cpr + kMxThreads - 1) / kMxThreads);
+    if (dtype == CSA_BF16)
+      k_quantize_mxfp4<__nv_bfloat16><<<ctas, kMxThreads, 0, s>>>(
+          (const __nv_bfloat16*)rows + i0 * row_stride, row_stride, m, cpr, slots, i0, out_rows,
+          codes, scales, (__nv_bfloat16*)values);
+    else
+      k_quantize_mxfp4<float><<<ctas, kMxThreads, 0, s>>>((const float*)rows + i0 * row_stride,
+                                                          row_stride, m, cpr, slots, i0, out_rows,
+                                                          codes, scales, (float*)values);
+    CSA_CHECK(launched("k_quantize_mxfp4"));
+  }
+  return CSA_OK;
+}
+
+// The pool and page table of a paged cache.
+static csa_status_t page_map(PageMap& pm, const int32_t* page_table, int32_t table_width,
+                             int32_t n_pages, int32_t page_size) {
+  if (page_size < 8 || page_size > (1 << 20) || (page_size & (page_size - 1)))
+    return fail(CSA_ERR_UNSUPPORTED_SHAPE, "page_size=%d: a power of two in [8, 2^20]", page_size);
+  if (table_width < 0 || n_pages < 0 || (long long)table_width * page_size > 2147483647LL ||
+      (long long)n_pages * page_size > 2147483647LL)
+    return fail(CSA_ERR_UNSUPPORTED_SHAPE,
+                "table_width=%d n_pages=%d page_size=%d: at most 2^31 - 1 rows each", table_width,
+                n_pages, page_size);
+  CSA_CHECK(check_ptr(page_table, "page_table", table_width == 0));
+  pm.table = page_table;
+  pm.width = table_width;
+  pm.n_pages = n_pages;
+  pm.shift = 0;
+  while ((1 << pm.shift) < page_size) ++pm.shift;
+  return CSA_OK;
+}
+
+static csa_status_t index_mx_checks(const csa_params_t* p, const uint8_t* q_codes,
+                                    const uint8_t* q_scales, const float* w,
+                                    const uint8_t* k_codes, const uint8_t* k_scales,
+                                    const int32_t* page_table, int32_t table_width,
+                                    int32_t n_pages, int32_t page_size, const int32_t* q_pos,
+                                    const int32_t* n_cmp, int32_t B, int32_t Tq, int32_t n_max,
+                                    PageMap& pm) {
+  CSA_CHECK(check_params(p));
+  CSA_CHECK(check_indexer_shape(p));
+  if (p->idx_dim & 31)
+    return fail(CSA_ERR_UNSUPPORTED_SHAPE, "idx_dim=%d: MXFP4 blocks need a multiple of 32",
+                p->idx_dim);
+  CSA_CHECK(check_sizes(B, Tq, n_max));
+  const bool none = n_max == 0;
+  if (table_width == 0 && page_table == nullptr) {  // contiguous: k rows [B][n_max]
+    if ((long long)B * n_max > 2147483647LL)
+      return fail(CSA_ERR_UNSUPPORTED_SHAPE, "B=%d n_max=%d: at most 2^31 - 1 keys", B, n_max);
+    pm = PageMap{nullptr, 0, 0, 0};
+  } else {
+    CSA_CHECK(page_map(pm, page_table, table_width, n_pages, page_size));
+    if (n_max > (long long)table_width * page_size)
+      return fail(CSA_ERR_INVALID_ARGUMENT, "n_max=%d beyond the page table's %lld entries", n_max,
+                  (long long)table_width * page_size);
+  }
+  CSA_CHECK(check_ptr(q_codes, "q_codes"));
+  CSA_CHECK(check_ptr(q_scales, "q_scales"));
+  CSA_CHECK(check_ptr(w, "w"));
+  CSA_CHECK(check_ptr(k_codes, "k_codes", none || (pm.table && n_pages == 0)));
+  CSA_CHECK(check_ptr(k_scales, "k_scales", none || (pm.table && n_pages == 0)));
+  CSA_CHECK(check_ptr(q_pos, "q_pos"));
+  return check_ptr(n_cmp, "n_cmp");
+}
+
+static csa_status_t index_mx_impl(const csa_params_t* p, const uint8_t* q_codes,
+                                  const uint8_t* q_scales, const float* w, const uint8_t* k_codes,
+                                  const uint8_t* k_scales, const PageMap& pm,
+                                  const int32_t* q_pos, const int32_t* n_cmp, int32_t B, int32_t Tq,
+                                  int32_t n_max, float* scores, cudaStream_t s) {
+  if (n_max == 0) return CSA_OK;
+  const int H_I = p->idx_heads, d_I = p->idx_dim;
+  if (Tq > 65535 || B > 65535) return fail(CSA_ERR_UNSUPPORTED_SHAPE, "B=%d Tq=%d", B, Tq);
+  dim3 grid((unsigned)(((long long)n_max + 127) / 128), (unsigned)Tq, (unsigned)B);
+  const size_t smem = (size_t)(H_I * d_I + H_I) * sizeof(float);
+  // the largest shape the indexer takes (16,384 dims and up to 512 heads)
+  CSA_CHECK(set_smem_attr(k_index_scores_mx_simt, (16384 + 512) * sizeof(float),
+                          "k_index_scores_mx_simt"));
+  k_index_scores_mx_simt<<<grid, 128, smem, s>>>(q_codes, q_scales, w, k_codes, k_scales, pm, q_pos,
+                                                 n_cmp, Tq, n_max, H_I, d_I, p->width, p->stride,
+                                                 scores);
+  return launched("k_index_scores_mx_simt");
+}
+
+CSA_API csa_status_t csa_index_scores_mxfp4(const csa_params_t* p, const uint8_t* q_codes,
+                                            const uint8_t* q_scales, const float* w,
+                                            const uint8_t* k_codes, const uint8_t* k_scales,
+                                            const int32_t* page_table, int32_t table_width,
+                                            int32_t n_pages, int32_t page_size,
+                                            const int32_t* q_pos, const int32_t* n_cmp, int32_t B,
+                                            int32_t Tq, int32_t n_max, float* scores,
+                                            void* stream) {
+  const CallRange trace("csa_index_scores_mxfp4");
+  PageMap pm;
+  CSA_CHECK(index_mx_checks(p, q_codes, q_scales, w, k_codes, k_scales, page_table, table_width,
+                            n_pages, page_size, q_pos, n_cmp, B, Tq, n_max, pm));
+  CSA_CHECK(check_ptr(scores, "scores", n_max == 0));
+  CSA_CHECK(check_device());
+  return index_mx_impl(p, q_codes, q_scales, w, k_codes, k_scales, pm, q_pos, n_cmp, B, Tq, n_max,
+                       scores, (cudaStream_t)stream);
+}
+
+CSA_API csa_status_t csa_index_topk_mxfp4(const csa_params_t* p, const uint8_t* q_codes,
+                                          const uint8_t* q_scales, const float* w,
+                                          const uint8_t* k_codes, const uint8_t* k_scales,
+                                          const int32_t* page_table, int32_t table_width,
+                                          int32_t n_pages, int32_t page_size, const int32_t* q_pos,
+                                          const int32_t* n_cmp, int32_t B, int32_t Tq,
+                                          int32_t n_max, int32_t* idx_out, void* ws,
+                                          size_t ws_bytes, void* stream) {
+  const CallRange trace("csa_index_topk_mxfp4");
+  PageMap pm;
+  CSA_CHECK(index_mx_checks(p, q_codes, q_scales, w, k_codes, k_scales, page_table, table_width,
+                            n_pages, page_size, q_pos, n_cmp, B, Tq, n_max, pm));
+  CSA_CHECK(check_topk(p));
+  CSA_CHECK(check_ptr(idx_out, "idx_out"));
+  const size_t sb = scores_bytes(B, Tq, n_max);
+  const size_t need = sb + topk_ws_bytes(p, B, Tq, n_max);
+  if (need > 0) CSA_CHECK(check_ptr(ws, "ws"));
+  if (ws_bytes < need)
+    return fail(CSA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes, need %zu", ws_bytes, need);
+  CSA_CHECK(check_device());
+  cudaStream_t s = (cudaStream_t)stream;
+  float* scores = (float*)ws;
+  CSA_CHECK(index_mx_impl(p, q_codes, q_scales, w, k_codes, k_scales, pm, q_pos, n_cmp, B, Tq,
+                          n_max, scores, s));
+  return topk_impl(p, scores, q_pos, n_cmp, B, Tq, n_max, idx_out, (char*)ws + sb, ws_bytes - sb,
+                   s);
+}
+
+template <bool kHca, typename T, int NK, int HG>
+static csa_status_t launch_paged_simt(const PagedAttnArgs& a, int tokens, cudaStream_t s) {
+  const long long gx = (long long)((a.H + HG - 1) / HG) * a.splits;
+  k_attn_paged_simt<T, kHca, NK, HG><<<dim3((unsigned)gx, (unsigned)tokens), 32 * kPgWarps, 0, s>>>(a);
+  CSA_CHECK(launched("k_attn_paged_simt"));
+  if (a.splits == 1) return CSA_OK;
+  k_attn_paged_join<T, NK><<<dim3((unsigned)a.H, (unsigned)tokens), 32, 0, s>>>(a);
+  return launched("k_attn_paged_join");
+}
+
+template <bool kHca>
+static csa_status_t paged_attn_simt(const csa_params_t* p, csa_dtype_t dtype, const AttnArgs& g,
+                                    const PageMap& pm, void* ws, size_t ws_bytes, cudaStream_t s) {
+  PagedAttnArgs a{};
+  a.q = g.q;
+  a.q_pos = g.q_pos;
+  a.kv = g.kv_cmp;
+  a.pm = pm;
+  a.idx = g.idx;
+  a.n_cmp = g.n_cmp;
+  a.n_max = g.n_max;
+  a.kv_raw = g.kv_raw;
+  a.raw_pos0 = g.raw_pos0;
+  a.n_raw = g.n_raw;
+  a.raw_max = g.raw_max;
+  a.sink = g.sink;
+  a.Tq = g.Tq;
+  a.H = g.H;
+  a.d = g.d;
+  a.rope_dim = g.rope_dim;
+  a.topk = g.topk;
+  a.window = g.window;
+  a.width = g.width;
+  a.stride = g.stride;
+  a.splits = paged_simt_splits(p, kHca, g.B, g.Tq, g.n_max);
+  a.scale = g.scale;
+  a.out = g.out;
+  const size_t need = paged_simt_ws_bytes(p, kHca, g.B, g.Tq, g.n_max);
+  if (ws_bytes < need)
+    return fail(CSA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes, need %zu", ws_bytes, need);
+  if (need > 0) CSA_CHECK(check_ptr(ws, "ws"));
+  a.part = (float*)ws;
+  for (int i = 0; i < g.rope_dim / 2; ++i) a.freq[i] = rope_freq(g.rope, i);
+  const int tokens = g.B * g.Tq;
+#define CSA_PAGED_CASE(D, NKV, HGV)                                                  \
+  case D:                                                                            \
+    return dtype == CSA_BF16 ? launch_paged_simt<kHca, __nv_bfloat16, NKV, HGV>(a, tokens, s) \
+                             : launch_paged_simt<kHca, float, NKV, HGV>(a, tokens, s);
+  switch (g.d) {
+    CSA_PAGED_CASE(64, 2, 8)
+    CSA_PAGED_CASE(128, 4, 8)
+    CSA_PAGED_CASE(256, 8, 4)
+    CSA_PAGED_CASE(512, 16, 2)
+    CSA_PAGED_CASE(1024, 32, 1)
+  }
+#undef CSA_PAGED_CASE
+  return fail(CSA_ERR_UNSUPPORTED_SHAPE, "d=%d", g.d);
+}
+
+static csa_status_t paged_attn_checks(const csa_params_t* p, csa_dtype_t dtype, const void* q,
+                                      const int32_t* q_pos, const void* kv_pages, int32_t n_pages,
+                                      int32_t page_size, const int32_t* page_table,
+                                      int32_t table_width, const void* kv_raw,
+                                      const int32_t* raw_pos0, const int32_t* n_raw,
+                                      int32_t raw_max, const float* sink, int32_t B, int32_t Tq,
+                                      void* out, PageMap& pm) {
+  CSA_CHECK(page_map(pm, page_table, table_width, n_pages, page_size));
+  CSA_CHECK(attn_common_checks(p, dtype, q, q_pos, n_pages == 0 ? q : kv_pages,
+                               table_width * page_size, kv_raw, raw_pos0, n_raw, raw_max, sink, B,
+                               Tq, out));
+  return CSA_OK;
+}
+
+CSA_API csa_status_t csa_sparse_attn_paged(const csa_params_t* p, csa_dtype_t dtype, const void* q,
+                                           const int32_t* q_pos, const void* kv_pages,
+                                           int32_t n_pages, int32_t page_size,
+                                           const int32_t* page_table, int32_t table_width,
+                                           const int32_t* idx, const void* kv_raw,
+                                           const int32_t* raw_pos0, const int32_t* n_raw,
+                                           int32_t raw_max, const float* sink, int32_t B,
+                                           int32_t Tq, void* out, void* ws, size_t ws_bytes,
+                                           void* stream) {
+  const CallRange trace("csa_sparse_attn_paged");
+  PageMap pm;
+  CSA_CHECK(paged_attn_checks(p, dtype, q, q_pos, kv_pages, n_pages, page_size, page_table,
+                              table_width, kv_raw, raw_pos0, n_raw, raw_max, sink, B, Tq, out, pm));
+  CSA_CHECK(check_topk(p));
+  CSA_CHECK(check_ptr(idx, "idx"));
+  CSA_CHECK(check_device());
+  AttnArgs a = make_attn_args(p, q, q_pos, kv_pages, idx, nullptr, table_width * page_size, kv_raw,
+                              raw_pos0, n_raw, raw_max, sink, B, Tq, out);
+  return paged_attn_simt<false>(p, dtype, a, pm, ws, ws_bytes, (cudaStream_t)stream);
+}
+
+CSA_API csa_status_t hca_attn_paged(const csa_params_t* p, csa_dtype_t dtype, const void* q,
+                                    const int32_t* q_pos, const void* kv_pages, int32_t n_pages,
+                                    int32_t page_size, const int32_t* page_table,
+                                    int32_t table_width, const int32_t* n_cmp, const void* kv_raw,
+                                    const int32_t* raw_pos0, const int32_t* n_raw, int32_t raw_max,
+                                    const float* sink, int32_t B, int32_t Tq, void* out, void* ws,
+                                    size_t ws_bytes, void* stream) {
+  const CallRange trace("hca_attn_paged");
+  PageMap pm;
+  CSA_CHECK(paged_attn_checks(p, dtype, q, q_pos, kv_pages, n_pages, page_size, page_table,
+                              table_width, kv_raw, raw_pos0, n_raw, raw_max, sink, B, Tq, out, pm));
+  CSA_CHECK(check_ptr(n_cmp, "n_cmp"));
+  CSA_CHECK(check_device());
+  AttnArgs a = make_attn_args(p, q, q_pos, kv_pages, nullptr, n_cmp, table_width * page_size,
+                              kv_raw, raw_pos0, n_raw, raw_max, sink, B, Tq, out);
+  return paged_attn_simt<true>(p, dtype, a, pm, ws, ws_bytes, (cudaStream_t)stream);
 }
 
 // ---------------------------------------------------------------------------

@@ -8,6 +8,10 @@ call the C ABI.  Every step runs in the CUDA library.
     CSA2 reuse layer: reuse_attn(p, q, ..., kv_cmp, idx, ...) -> out
     decode-time append: append_tokens(p, x, gate, x_pos0, t_old, t_new, ...)
     FP8 caches: quantize_fp8(rows) -> (codes, scales); csa_decode_fp8(...)
+    norm + RoPE of heads: norm_rope(p, q, ...) -> (q_out, k_out)
+    paged caches: csa_decode_paged(...) with the indexer in 4 bits,
+    sparse_attn_paged(...), hca_decode_paged(...); quantize_mxfp4(rows) ->
+    (codes, scales)
 """
 from __future__ import annotations
 
@@ -159,3 +163,83 @@ def csa_decode_fp8(p: L.Params, q, q_pos, q_idx, w, k_idx, n_cmp, kv_cmp, cmp_sc
     L.csa_sparse_attn_fp8(p, q, q_pos, kv_cmp, cmp_scale, idx, kv_raw, raw_scale, raw_pos0, n_raw,
                           sink, out, ws.get(nb), stream)
     return idx, out
+
+
+def norm_rope(p: L.Params, q, q_weight=None, q_pos=None, k=None, k_weight=None, k_pos=None,
+              k_out=None, k_slots=None, eps: float = 1e-6, stream=None):
+    """RMS norm of every head of q [rows][heads][dim] (and k) and rotation of
+    the trailing p.rope_dim dims by q_pos (k_pos), in one pass: the indexer's
+    queries and keys, token rows, or pooled entries on their way to a cache.
+    Returns (q_out, k_out); with k_out and k_slots given, row r of k goes to
+    row k_slots[r] of k_out."""
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k is not None and k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    L.csa_norm_rope(p, eps, q, q_weight, q_pos, q_out, k, k_weight, k_pos, k_out, k_slots, stream)
+    return q_out, k_out
+
+
+def quantize_mxfp4(rows, stream=None):
+    """Rows [..., d] -> (E2M1 codes uint8 [..., d / 2], E8M0 scales uint8
+    [..., d / 32]), one scale per 32 values."""
+    codes = torch.empty(rows.shape[:-1] + (rows.shape[-1] // 2,), dtype=torch.uint8,
+                        device=rows.device)
+    scales = torch.empty(rows.shape[:-1] + (rows.shape[-1] // 32,), dtype=torch.uint8,
+                         device=rows.device)
+    L.csa_quantize_mxfp4(rows, codes, scales, stream=stream)
+    return codes, scales
+
+
+def sparse_attn_paged(p: L.Params, q, q_pos, kv_pages, page_table, idx, kv_raw, raw_pos0, n_raw,
+                      sink, ws: Workspace | None = None, out=None, stream=None):
+    """Attention over the selected entries idx [B][Tq][topk] of a paged cache
+    kv_pages [n_pages][page][d] and the window's raw rows."""
+    ws = ws or Workspace(q.device)
+    if out is None:
+        out = torch.empty_like(q)
+    B, Tq = q_pos.shape
+    nb = L.csa_workspace_size(p, L.CSA_OP_SPARSE_ATTN_PAGED, B, Tq,
+                              page_table.shape[1] * kv_pages.shape[1])
+    L.csa_sparse_attn_paged(p, q, q_pos, kv_pages, page_table, idx, kv_raw, raw_pos0, n_raw, sink,
+                            out, ws.get(nb), stream)
+    return out
+
+
+def hca_decode_paged(p: L.Params, q, q_pos, kv_pages, page_table, n_cmp, kv_raw, raw_pos0, n_raw,
+                     sink, ws: Workspace | None = None, out=None, stream=None):
+    """HCA decode over a paged entry cache of any length; with
+    Params(width=1, stride=1) every token is its own entry."""
+    ws = ws or Workspace(q.device)
+    if out is None:
+        out = torch.empty_like(q)
+    B, Tq = q_pos.shape
+    nb = L.csa_workspace_size(p, L.CSA_OP_HCA_ATTN_PAGED, B, Tq,
+                              page_table.shape[1] * kv_pages.shape[1])
+    L.hca_attn_paged(p, q, q_pos, kv_pages, page_table, n_cmp, kv_raw, raw_pos0, n_raw, sink, out,
+                     ws.get(nb), stream)
+    return out
+
+
+def csa_decode_paged(p: L.Params, q, q_pos, q_idx, w, k_codes, k_scales, n_cmp, kv_pages,
+                     page_table, kv_raw, raw_pos0, n_raw, sink, ws: Workspace | None = None,
+                     idx=None, out=None, n_max: int | None = None, stream=None):
+    """CSA decode over paged caches with the indexer in 4 bits: q_idx
+    [B][Tq][H_I][d_I] (after its norm and rotation) is quantized to MXFP4,
+    scored against the paged MXFP4 keys, and the top-k entries of the paged
+    entry cache attended to.  The key and entry pools share page_table; n_max
+    bounds the entries scored (None: all the table holds)."""
+    if k_codes.shape[1] != kv_pages.shape[1]:
+        raise ValueError(f"the pools share a page table: pages of {k_codes.shape[1]} keys and "
+                         f"{kv_pages.shape[1]} entries")
+    ws = ws or Workspace(q.device)
+    B, Tq = q_pos.shape
+    if idx is None:
+        idx = torch.empty((B, Tq, p.topk), dtype=torch.int32, device=q.device)
+    q_codes, q_scales = quantize_mxfp4(q_idx, stream)
+    if n_max is None:
+        n_max = page_table.shape[1] * k_codes.shape[1]
+    nb = L.csa_workspace_size(p, L.CSA_OP_INDEX_TOPK, B, Tq, n_max)
+    L.csa_index_topk_mxfp4(p, q_codes, q_scales, w, k_codes, k_scales, page_table, q_pos, n_cmp,
+                           idx, ws.get(nb), n_max, stream)
+    return idx, sparse_attn_paged(p, q, q_pos, kv_pages, page_table, idx, kv_raw, raw_pos0, n_raw,
+                                  sink, ws, out, stream)

@@ -1,0 +1,301 @@
+"""Attention over paged caches against the fp64 oracle, at the layer's own
+bounds (bf16: max-abs 2e-2 and relative L2 5e-3; fp32: 1e-5).  The pool's
+unused rows hold NaN and unused table entries a page outside the pool."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from gpu_util import assert_close, host64
+from sparse_compressed_attention_csa_b200 import (CSA_OP_HCA_ATTN_PAGED, CsaError, Params,
+                                                  csa_poll_device_error, csa_workspace_size,
+                                                  hca_attn_paged, layer)
+from test_gpu_mxfp4 import paged
+
+pytestmark = pytest.mark.gpu
+I32 = torch.int32
+
+
+def _case(dtype, H, d, rope, lens, Tq, page, width, stride, window, seed, topk=0, keep_raw=None,
+          scale_q=1.0):
+    rng = np.random.default_rng(seed)
+    tdt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    val = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float32)).to(tdt)  # noqa: E731
+    B = len(lens)
+    n_cmp = [oracle.n_compressed(t, width, stride) for t in lens]
+    kv = [val(n, d) for n in n_cmp]
+    raw_max = max(1, window + Tq if keep_raw is None else keep_raw)
+    raw = val(B, raw_max, d)
+    pos0 = [max(0, t - raw_max) for t in lens]
+    n_raw = [min(t, raw_max) for t in lens]
+    for b in range(B):
+        raw[b, n_raw[b]:] = float("nan")
+    q = val(B, Tq, H, d) * scale_q
+    sink = rng.standard_normal(H).astype(np.float32)
+    q_pos = np.array([[t - Tq + i for i in range(Tq)] for t in lens], dtype=np.int32)
+    pool, table = paged([k.float().numpy() for k in kv], page, seed, np.nan)
+    c = lambda a, dt: torch.as_tensor(a).to(dt).cuda()  # noqa: E731
+    t = dict(q=q.cuda(), q_pos=c(q_pos, I32), kv=c(pool, tdt), table=c(table, I32), raw=raw.cuda(),
+             pos0=c(pos0, I32), n_raw=c(n_raw, I32), sink=c(sink, torch.float32), n_cmp=c(n_cmp, I32))
+    p = Params(d=d, rope_dim=rope, n_heads=H, topk=max(topk, 1), window=window, width=width, stride=stride)
+    idx = None
+    if topk:
+        idx = np.full((B, Tq, topk), -1, dtype=np.int32)
+        for b in range(B):
+            for i in range(Tq):
+                n = oracle.n_visible(int(q_pos[b, i]), n_cmp[b], width, stride)
+                pick = np.sort(rng.permutation(n)[:topk])
+                idx[b, i, :len(pick)] = pick
+        t["idx"] = c(idx, I32)
+    scale = 1.0 / np.sqrt(d)
+    want = []
+    for b in range(B):
+        f = lambda a: a.double().numpy()  # noqa: E731
+        args = (f(raw[b]), pos0[b], n_raw[b], sink, scale, window)
+        if topk:
+            want.append(oracle.sparse_attn(f(q[b]), q_pos[b], f(kv[b]), idx[b], *args, rope, 1e4))
+        else:
+            want.append(oracle.hca_attn(f(q[b]), q_pos[b], f(kv[b]), n_cmp[b], *args, width, stride, rope, 1e4))
+    return p, t, np.stack(want)
+
+
+def _hca(p, t, **kw):
+    return layer.hca_decode_paged(p, t["q"], t["q_pos"], t["kv"], t["table"], t["n_cmp"], t["raw"], t["pos0"],
+                                  t["n_raw"], t["sink"], **kw)
+
+
+def _sparse(p, t, **kw):
+    return layer.sparse_attn_paged(p, t["q"], t["q_pos"], t["kv"], t["table"], t["idx"], t["raw"], t["pos0"],
+                                   t["n_raw"], t["sink"], **kw)
+
+
+HCA = [
+    # dtype, H, d, rope, lens, Tq, page, width, stride, window
+    ("bf16", 128, 512, 64, [1], 1, 64, 1, 1, 0),
+    ("bf16", 128, 512, 64, [64, 65, 63, 1], 1, 8, 1, 1, 0),
+    ("bf16", 128, 512, 64, [2000, 37], 1, 16, 1, 1, 0),
+    ("bf16", 128, 512, 64, [40000, 5, 129 * 128], 1, 64, 128, 128, 128),
+    ("bf16", 128, 512, 64, [9001, 300, 4097], 2, 32, 1, 1, 128),
+    ("bf16", 128, 512, 64, [30000], 1, 128, 1, 1, 16),
+    ("bf16", 128, 512, 128, [3000, 2999], 1, 256, 4, 4, 100),
+    ("bf16", 128, 512, 0, [777], 3, 64, 1, 1, 128),
+    ("bf16", 16, 512, 64, [5000, 17], 1, 64, 1, 1, 128),
+    ("bf16", 64, 512, 64, [3000], 2, 64, 2, 2, 128),
+    ("bf16", 5, 512, 64, [1300, 2], 1, 64, 1, 1, 8),
+    ("bf16", 200, 512, 64, [900, 64], 1, 64, 1, 1, 128),
+    ("bf16", 128, 512, 64, [100] * 9, 7, 64, 1, 1, 20),
+    ("bf16", 128, 512, 64, [10, 90, 100, 127], 1, 64, 128, 128, 128),     # no entry yet
+    ("bf16", 128, 512, 64, [700] * 160, 1, 64, 1, 1, 0),
+    ("bf16", 3, 64, 32, [500, 1], 1, 16, 1, 1, 16),
+    ("bf16", 8, 128, 64, [5000], 2, 64, 1, 1, 128),
+    ("bf16", 4, 256, 64, [700], 1, 8, 1, 1, 0),
+    ("bf16", 2, 1024, 64, [700], 1, 64, 1, 1, 3),
+    ("f32", 3, 64, 32, [256, 9, 100], 2, 8, 4, 4, 16),
+    ("f32", 8, 128, 64, [3000], 1, 64, 1, 1, 0),
+    ("f32", 128, 512, 64, [400, 130], 1, 64, 1, 1, 128),
+    ("f32", 1, 1024, 0, [90], 1, 16, 1, 1, 4),
+]
+
+
+@pytest.mark.parametrize("c", HCA, ids=lambda c: str(c)[:60])
+def test_hca_paged(c):
+    p, t, want = _case(*c, seed=HCA.index(c))
+    out = _hca(p, t)
+    torch.cuda.synchronize()
+    csa_poll_device_error()
+    assert_close(host64(out), want, c[0], str(c))
+
+
+SPARSE = [
+    # dtype, H, d, rope, lens, Tq, page, width, stride, window, topk
+    ("bf16", 128, 512, 64, [20000, 5003], 1, 64, 8, 4, 128, 1024),
+    ("bf16", 128, 512, 64, [5003, 2001, 40], 2, 16, 8, 4, 128, 1024),
+    ("bf16", 128, 512, 64, [3000], 1, 8, 2, 2, 128, 512),
+    ("bf16", 128, 512, 64, [9000] * 3, 1, 256, 8, 4, 0, 64),
+    ("bf16", 128, 512, 64, [7, 3, 9], 1, 64, 8, 4, 128, 64),
+    ("bf16", 128, 512, 64, [30000], 1, 64, 8, 4, 128, 4096),              # past one pair's row list
+    ("bf16", 16, 512, 64, [3000], 1, 64, 8, 4, 128, 256),
+    ("f32", 3, 64, 32, [256, 20], 2, 16, 8, 4, 5, 7),
+    ("f32", 8, 128, 64, [3000], 1, 64, 8, 4, 128, 100),
+]
+
+
+@pytest.mark.parametrize("c", SPARSE, ids=str)
+def test_sparse_paged(c):
+    p, t, want = _case(*c[:10], seed=50 + SPARSE.index(c), topk=c[10])
+    out = _sparse(p, t)
+    torch.cuda.synchronize()
+    csa_poll_device_error()
+    assert_close(host64(out), want, c[0], str(c))
+
+
+def test_paged_agrees_with_a_contiguous_cache():
+    # the same rows through pages and from a contiguous cache
+    from sparse_compressed_attention_csa_b200 import CSA_OP_SPARSE_ATTN, csa_sparse_attn
+    p, t, _ = _case("bf16", 128, 512, 64, [9000, 4001], 1, 64, 8, 4, 128, 70, topk=1024)
+    n_max = t["table"].shape[1] * 64
+    flat = torch.zeros(2, n_max, 512, dtype=torch.bfloat16, device="cuda")
+    for b in range(2):
+        n = int(t["n_cmp"][b])
+        flat[b, :n] = t["kv"][t["table"][b, :-(-n // 64)].long()].flatten(0, 1)[:n]
+    out = torch.empty_like(t["q"])
+    ws = torch.empty(max(256, csa_workspace_size(p, CSA_OP_SPARSE_ATTN, 2, 1, n_max)), dtype=torch.uint8,
+                     device="cuda")
+    csa_sparse_attn(p, t["q"], t["q_pos"], flat, t["idx"], t["raw"], t["pos0"], t["n_raw"], t["sink"], out, ws)
+    got = _sparse(p, t)
+    assert_close(host64(got), host64(out), "bf16", "paged against contiguous")
+
+
+def test_large_logits_and_sinks():
+    # one row dominates (the running maximum moves far), and sinks of +-inf scale
+    p, t, want = _case("bf16", 128, 512, 64, [3000, 70], 1, 64, 1, 1, 128, 71, scale_q=6.0)
+    out = _hca(p, t)
+    assert_close(host64(out), want, "bf16", "large logits")
+    t["sink"].fill_(-float("inf"))
+    out = _hca(p, t)
+    assert torch.isfinite(out).all()
+    # nothing visible, no window and no sink: zeros
+    p0 = Params(window=0, width=128, stride=128)
+    t["q_pos"].fill_(5)
+    out = _hca(p0, t)
+    assert torch.all(out == 0)
+    csa_poll_device_error()
+
+
+@pytest.mark.parametrize("H,d,dtype", [(128, 512, "bf16"), (3, 64, "f32")])
+def test_pages_outside_the_pool_are_reported_and_skipped(H, d, dtype):
+    rope = 64 if d == 512 else 32
+    p, t, want = _case(dtype, H, d, rope, [1000, 640], 1, 16, 1, 1, 0, 72)
+    t["table"][0, 2] = -1                                   # entries 32 .. 47 of sequence 0
+    t["table"][0, 40] = t["kv"].shape[0]                    # entries 640 .. 655
+    out = _hca(p, t)
+    with pytest.raises(CsaError) as ei:
+        csa_poll_device_error()
+    assert ei.value.status == 8
+    n = 1000
+    keep = [j for j in range(n) if not (32 <= j < 48 or 640 <= j < 656)]
+    rows = t["kv"].flatten(0, 1).double().cpu().numpy()
+    tab = t["table"][0].cpu().numpy().astype(np.int64)
+    ent = np.stack([rows[tab[j // 16] * 16 + j % 16] for j in keep])
+    want0 = oracle.attend(t["q"][0, 0].double().cpu().numpy(), 999, ent, t["sink"].cpu().numpy(),
+                          1 / np.sqrt(d), rope, 1e4)
+    assert_close(host64(out)[0, 0], want0, dtype, "bad pages")
+    assert_close(host64(out)[1], want[1], dtype, "the other sequence")
+
+
+def test_bad_selection_pages_are_reported_and_skipped():
+    p, t, want = _case("bf16", 128, 512, 64, [4000, 4000], 1, 16, 8, 4, 128, 73, topk=128)
+    t["table"][0, int(t["idx"][0, 0, 5]) // 16] = -3
+    t["idx"][0, 0, 9] = t["table"].shape[1] * 16
+    out = _sparse(p, t)
+    with pytest.raises(CsaError) as ei:
+        csa_poll_device_error()
+    assert ei.value.status == 8
+    assert torch.isfinite(out).all()
+    assert_close(host64(out)[1], want[1], "bf16", "the other sequence")
+
+
+def test_results_repeat_in_place_on_streams_and_from_two_graphs():
+    p, t, want = _case("bf16", 128, 512, 64, [9000, 41, 4000], 1, 64, 1, 1, 128, 74)
+    first = _hca(p, t)
+    assert_close(host64(first), want, "bf16", "first")
+    for _ in range(5):
+        assert torch.equal(_hca(p, t), first)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        a = _hca(p, t)
+    side.synchronize()
+    assert torch.equal(a, first)
+    # two graphs that share a workspace, replayed one after the other
+    ws = layer.Workspace("cuda")
+    outs = [torch.zeros_like(first) for _ in range(2)]
+    _hca(p, t, ws=ws, out=outs[0])
+    torch.cuda.synchronize()
+    graphs = []
+    for o in outs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            _hca(p, t, ws=ws, out=o)
+        graphs.append(g)
+    for _ in range(2):
+        for o in outs:
+            o.zero_()
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, first) for o in outs)
+    csa_poll_device_error()
+
+
+def test_workspace_too_small_is_refused():
+    p, t, _ = _case("bf16", 128, 512, 64, [9000], 1, 64, 1, 1, 0, 75)
+    nb = csa_workspace_size(p, CSA_OP_HCA_ATTN_PAGED, 1, 1, t["table"].shape[1] * 64)
+    assert nb > 0
+    with pytest.raises(CsaError) as ei:
+        hca_attn_paged(p, t["q"], t["q_pos"], t["kv"], t["table"], t["n_cmp"], t["raw"], t["pos0"], t["n_raw"],
+                       t["sink"], torch.empty_like(t["q"]), torch.empty(nb - 16, dtype=torch.uint8, device="cuda"))
+    assert ei.value.status == 5
+
+
+def test_a_decode_step_through_every_operator():
+    """Norm and rotation of new keys and entries into pages, 4-bit keys, then
+    the decode over both caches: each step against the oracle on what the
+    step before it gave."""
+    rng = np.random.default_rng(76)
+    B, T, page, topk = 3, [2600, 1411, 90], 32, 256
+    p = Params(topk=topk)
+    bf = torch.bfloat16
+    n_cmp = [oracle.n_compressed(t, 8, 4) for t in T]
+    per = [-(-n // page) for n in n_cmp]
+    table = np.zeros((B, max(per)), dtype=np.int32)
+    order, at = rng.permutation(sum(per)), 0
+    for b in range(B):
+        table[b, :per[b]] = order[at:at + per[b]]
+        at += per[b]
+    slots = np.concatenate([table[b][np.arange(n) // page] * page + np.arange(n) % page for b, n in enumerate(n_cmp)])
+    pos = np.concatenate([4 * np.arange(n) for n in n_cmp])
+    c = lambda a: torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).cuda()  # noqa: E731
+    val = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float32)).cuda().to(bf)  # noqa: E731
+    N = len(slots)
+    keys, entries = val(N, 1, 128), val(N, 1, 512)
+    q_idx, q = val(B, 64, 128), val(B, 128, 512)
+    kw, qw = 1 + 0.1 * torch.randn(128, device="cuda"), 1 + 0.1 * torch.randn(128, device="cuda")
+    q_pos = np.array([[t - 1] for t in T], dtype=np.int32)
+    slots_d, pos_d = c(slots), c(pos)
+    # caches: normed and rotated entries straight into pages; keys normed, rotated, quantized into pages
+    kv = torch.full((sum(per), page, 512), float("nan"), dtype=bf, device="cuda")
+    layer.norm_rope(p, q, None, None, entries, None, pos_d, kv.view(-1, 1, 512), slots_d)
+    q_idx_n, keys_n = layer.norm_rope(p, q_idx, qw, c(q_pos[:, 0]), keys, kw, pos_d)
+    k_codes = torch.zeros(sum(per), page, 64, dtype=torch.uint8, device="cuda")
+    k_scales = torch.full((sum(per), page, 4), 255, dtype=torch.uint8, device="cuda")
+    from sparse_compressed_attention_csa_b200 import csa_quantize_mxfp4
+    csa_quantize_mxfp4(keys_n[:, 0], k_codes, k_scales, slots=slots_d)
+    raw, w, sink = val(B, 128, 512), torch.rand(B, 1, 64, device="cuda"), torch.randn(128, device="cuda")
+    pos0 = c([max(0, t - 128) for t in T])
+    n_raw = c([min(t, 128) for t in T])
+    idx, out = layer.csa_decode_paged(p, q[:, None], c(q_pos), q_idx_n[:, None], w, k_codes, k_scales, c(n_cmp),
+                                      kv, c(table), raw, pos0, n_raw, sink)
+    torch.cuda.synchronize()
+    csa_poll_device_error()
+    at = 0
+    for b in range(B):
+        n = n_cmp[b]
+        ent = oracle.paged_rows(kv.float().cpu().numpy(), table[b], n)
+        ent_o = oracle.norm_rope(entries[at:at + n].double().cpu().numpy(), None, pos[at:at + n], 64, 1e4, 1e-6)[:, 0]
+        assert_close(ent, ent_o, "bf16", "entries in pages")
+        kc, ks = oracle.mxfp4_encode(keys_n[at:at + n, 0].double().cpu().numpy())
+        np.testing.assert_array_equal(oracle.paged_rows(k_codes.cpu().numpy(), table[b], n), kc)
+        qv = oracle.mxfp4_decode(*oracle.mxfp4_encode(q_idx_n[b].double().cpu().numpy()))
+        s = oracle.index_scores(qv[None], w[b].cpu().numpy(), oracle.mxfp4_decode(kc, ks))[0]
+        got = idx[b, 0].cpu().numpy()
+        got = got[got >= 0]
+        assert len(got) == min(topk, n) and np.all(np.diff(got) > 0)
+        if n > topk:  # every kept score reaches the k-th best, up to the fp32 sums
+            cut = np.sort(s)[-topk]
+            assert np.all(s[got] >= cut - 1e-4 * np.abs(s).max())
+        want = oracle.sparse_attn(q[b:b + 1].double().cpu().numpy(), q_pos[b], ent, idx[b].cpu().numpy(),
+                                  raw[b].double().cpu().numpy(), int(pos0[b]), int(n_raw[b]), sink.cpu().numpy(),
+                                  1 / np.sqrt(512), 128, 64, 1e4)
+        assert_close(host64(out)[b], want, "bf16", "decode")
+        at += n
