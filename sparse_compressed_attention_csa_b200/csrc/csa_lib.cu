@@ -20,6 +20,7 @@
 #include "compress.cuh"
 #include "quantize.cuh"
 #include "csa.h"
+#include "indexer_mx.cuh"
 #include "indexer_simt.cuh"
 #include "indexer_tc.cuh"
 #include "mxfp4.cuh"
@@ -305,6 +306,21 @@ csa_status_t make_tmap_u8(CUtensorMap* m, const void* base, uint64_t inner, uint
   cuuint32_t estr[2] = {1, 1};
   CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides,
                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(CSA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return CSA_OK;
+}
+
+// Map over rows of 64 bytes (128 E2M1 codes), 64-byte swizzle.
+csa_status_t make_tmap_mx(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_rows) {
+  auto enc = tensor_map_encoder();
+  if (enc == nullptr) return fail(CSA_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+  cuuint64_t dims[2] = {(cuuint64_t)kImRow, rows};
+  cuuint64_t strides[1] = {(cuuint64_t)kImRow};
+  cuuint32_t box[2] = {(cuuint32_t)kImRow, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides,
+                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(CSA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   return CSA_OK;
@@ -1309,6 +1325,48 @@ static csa_status_t index_mx_checks(const csa_params_t* p, const uint8_t* q_code
   return check_ptr(n_cmp, "n_cmp");
 }
 
+template <int NT, int QU, int STAGES, int MINB>
+static csa_status_t launch_index_mx(const csa_params_t* p, const uint8_t* q_codes,
+                                    const uint8_t* q_scales, const float* w,
+                                    const uint8_t* k_codes, const uint8_t* k_scales,
+                                    const PageMap& pm, const int32_t* q_pos, const int32_t* n_cmp,
+                                    int32_t B, int32_t Tq, int32_t n_max, float* scores,
+                                    cudaStream_t s) {
+  IdxMxArgs a;
+  a.q_scales = q_scales;
+  a.w = w;
+  a.k_scales = k_scales;
+  a.pm = pm;
+  a.q_pos = q_pos;
+  a.n_cmp = n_cmp;
+  a.B = B;
+  a.Tq = Tq;
+  a.n_max = n_max;
+  a.width = p->width;
+  a.stride = p->stride;
+  a.blocks_q = (Tq + QU - 1) / QU;
+  a.units = a.blocks_q * B;
+  a.box_rows = pm.table != nullptr && pm.shift < 7 ? 1 << pm.shift : kImKeys;
+  a.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
+  a.scores = scores;
+  const int slots = MINB * num_sms();
+  a.planned = a.units <= std::min(slots, kImMaxPlan);
+  // a planned grid: no more CTAs than there can be key tiles
+  const long long tiles = (long long)a.units * ((n_max + kImKeys - 1) / kImKeys);
+  const int grid = a.planned ? (int)std::max<long long>(a.units, std::min<long long>(slots, tiles))
+                             : std::min(slots, a.units);
+  CUtensorMap tk, tq;
+  const uint64_t krows = pm.table != nullptr ? (uint64_t)pm.n_pages << pm.shift : (uint64_t)B * n_max;
+  CSA_CHECK(make_tmap_mx(&tk, k_codes, krows, (uint32_t)a.box_rows));
+  CSA_CHECK(make_tmap_mx(&tq, q_codes, (uint64_t)B * Tq * kImHeads, kImHeads));
+  auto kern = k_index_scores_mx<NT, QU, STAGES, MINB>;
+  const size_t smem = sizeof(IdxMxSmem<NT, QU, STAGES>) + 1024;
+  CSA_CHECK(set_smem_attr(kern, smem, "k_index_scores_mx"));
+  const cudaError_t e = launch_ex(kern, dim3((unsigned)grid), dim3(128 + 128 * NT), smem, s, 1, tk, tq, a);
+  if (e != cudaSuccess) return cuda_fail(e, "k_index_scores_mx");
+  return launched("k_index_scores_mx");
+}
+
 static csa_status_t index_mx_impl(const csa_params_t* p, const uint8_t* q_codes,
                                   const uint8_t* q_scales, const float* w, const uint8_t* k_codes,
                                   const uint8_t* k_scales, const PageMap& pm,
@@ -1316,7 +1374,15 @@ static csa_status_t index_mx_impl(const csa_params_t* p, const uint8_t* q_codes,
                                   int32_t n_max, float* scores, cudaStream_t s) {
   if (n_max == 0) return CSA_OK;
   const int H_I = p->idx_heads, d_I = p->idx_dim;
-  if (Tq > 65535 || B > 65535) return fail(CSA_ERR_UNSUPPORTED_SHAPE, "B=%d Tq=%d", B, Tq);
+  // tensor cores: the measured indexer shape; box coordinates are 32-bit
+  const bool pool = pm.table == nullptr || pm.n_pages > 0;
+  if (H_I == kImHeads && d_I == kImDim && pool) {
+    if (Tq == 1)
+      return launch_index_mx<1, 1, 8, 2>(p, q_codes, q_scales, w, k_codes, k_scales, pm, q_pos, n_cmp,
+                                         B, Tq, n_max, scores, s);
+    return launch_index_mx<2, 16, 6, 1>(p, q_codes, q_scales, w, k_codes, k_scales, pm, q_pos, n_cmp,
+                                        B, Tq, n_max, scores, s);
+  }
   dim3 grid((unsigned)(((long long)n_max + 127) / 128), (unsigned)Tq, (unsigned)B);
   const size_t smem = (size_t)(H_I * d_I + H_I) * sizeof(float);
   // the largest shape the indexer takes (16,384 dims and up to 512 heads)

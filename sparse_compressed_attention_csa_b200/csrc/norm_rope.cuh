@@ -45,17 +45,15 @@ struct NormRopeArgs {
   double freq[kNormMaxPairs];
 };
 
-// cos / sin of pos * freq to fp32 accuracy: the angle is reduced modulo 2 pi
-// in double precision (as rope_cs_reduced) and its rounding to fp32, up to
-// 2^-24 pi, is put back to first order.
+// cos / sin of pos * freq to fp32 accuracy: the angle in half turns is
+// reduced to [-1, 1] in double precision (error about 1e-16 of it), and what
+// rounding it to fp32 drops is put back to first order.
 __device__ __forceinline__ void norm_cos_sin(long long pos, double freq, float* c, float* s) {
-  const double x = (double)pos * freq;
-  const double k = rint(x * 0.15915494309189535);
-  double r = fma(-k, 6.283185307179586, x);
-  r = fma(-k, 2.4492935982947064e-16, r);
-  const float hi = (float)r, lo = (float)(r - (double)hi);
+  const double turns = (double)pos * freq * 0.15915494309189535;
+  const double half = 2.0 * (turns - rint(turns));
+  const float hi = (float)half, lo = 3.14159265f * (float)(half - (double)hi);
   float sh, ch;
-  sincosf(hi, &sh, &ch);
+  sincospif(hi, &sh, &ch);
   *s = fmaf(ch, lo, sh);
   *c = fmaf(-sh, lo, ch);
 }

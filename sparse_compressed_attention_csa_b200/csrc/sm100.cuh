@@ -146,6 +146,13 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool v
                : "memory");
 }
 
+// 4 bytes global -> shared, zero-filled when !valid.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+               "r"(valid ? 4 : 0)
+               : "memory");
+}
+
 // Arrive on `bar` (without raising its expected count) once every cp.async
 // this thread issued before has landed.
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
@@ -434,6 +441,64 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t smem_addr, uint32_t lbo_
   d |= (uint64_t)1 << 46;  // descriptor version of sm_100
   d |= (uint64_t)2 << 61;  // SWIZZLE_128B
   return d;
+}
+
+// Shared-memory matrix descriptor of a K-major operand with 64-byte rows
+// (64-byte swizzle): 8-row atoms of 512 B, sbo the distance between them.
+__device__ __forceinline__ uint64_t sw64_desc(uint32_t smem_addr, uint32_t sbo_bytes) {
+  uint64_t d = 0;
+  d |= (uint64_t)((smem_addr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)1 << 16;  // lbo, unused
+  d |= (uint64_t)((sbo_bytes >> 4) & 0x3FFFu) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)4 << 61;  // SWIZZLE_64B
+  return d;
+}
+
+// Descriptor of 32 rows of 16 bytes, contiguous (no swizzle; 8-row groups of
+// 128 B): the source of tc_cp_scales.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t smem_addr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((smem_addr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)8 << 32;  // sbo 128 B
+  d |= (uint64_t)1 << 46;
+  return d;
+}
+
+// Block scales shared memory -> TMEM: 32 rows of 16 bytes to four columns,
+// the same in each quarter of the lanes.  Row l's 32-bit word c holds the
+// four scales of operand row l + 32 c.  Ordered with the MMAs that this
+// thread issues after it.
+__device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+               : "memory");
+}
+
+// Instruction descriptor of kind::mxf4: E2M1 A and B (K-major), E8M0 scales,
+// fp32 accumulator.  sf: which half (0 or 2) of the 32-bit scale words holds
+// this K step's two scales.
+__host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, int sf) {
+  return ((uint32_t)sf << 4)              // B scales
+         | (1u << 7)                      // A format: E2M1
+         | (1u << 10)                     // B format: E2M1
+         | ((uint32_t)(N >> 3) << 17)     // N / 8
+         | (1u << 23)                     // scale format: E8M0
+         | ((uint32_t)(M >> 7) << 27)     // M / 128
+         | ((uint32_t)sf << 29);          // A scales
+}
+
+// D[tmem] (+)= (A * 2^sa) (B * 2^sb)^T over 64 values of K (kind::mxf4, one
+// scale per 32 values, scales in TMEM).
+__device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                         uint32_t idesc, uint32_t sa_tmem, uint32_t sb_tmem,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], "
+      "p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+      : "memory");
 }
 
 // 32 lanes x 32 consecutive 32-bit columns: thread i of the warp gets lane

@@ -112,7 +112,7 @@ def _score_case(lens, Tq, H, D, page, seed, width=8, stride=4, integer=False):
     w = np.exp2(rng.integers(-2, 3, (B, Tq, H))).astype(np.float32) * rng.choice([-1, 1], (B, Tq, H)).astype(np.float32)
     if not integer:
         w *= rng.uniform(0.5, 1.5, w.shape).astype(np.float32)
-    q_pos = np.array([[t - Tq + i for i in range(Tq)] for t in lens], dtype=np.int32)
+    q_pos = np.array([[max(0, t - Tq + i) for i in range(Tq)] for t in lens], dtype=np.int32)
     kcp, table = paged(list(kc), page, seed, 0x77)
     ksp, _ = paged(list(ksc), page, seed, 0xFF)               # NaN scales behind the last key
     c = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
@@ -153,7 +153,9 @@ def _check_scores(p, t, want, bound, vis, n_max, exact=False):
     ([520, 8], 8, 64, 128, 256), ([333], 333, 64, 128, 32), ([40000, 12, 33000], 1, 64, 128, 128),
     ([700], 2, 4, 32, 16), ([600, 90], 1, 5, 96, 64), ([4000], 1, 128, 128, 64), ([1000], 1, 64, 64, 64),
     ([2048], 5, 64, 128, 512), ([7], 1, 64, 128, 64),
-])
+    ([500 + 7 * (i % 90) for i in range(300)], 1, 64, 128, 64),   # more units than CTAs
+    ([2600], 2600, 64, 128, 32), ([900, 40, 1500], 33, 64, 128, 64),
+], ids=lambda v: str(v)[:24])
 def test_index_scores(lens, Tq, H, D, page):
     p = Params(idx_heads=H, idx_dim=D)
     t, want, bound, vis = _score_case(lens, Tq, H, D, page, sum(lens) + Tq)
