@@ -520,7 +520,8 @@ CSA_API csa_status_t csa_workspace_size(const csa_params_t* p, csa_op_t op, int3
     case CSA_OP_SPARSE_ATTN: *bytes = attn_ws_bytes(p, CSA_BF16, false, B, Tq, n_max); return CSA_OK;
     case CSA_OP_HCA_ATTN: *bytes = attn_ws_bytes(p, CSA_BF16, true, B, Tq, n_max); return CSA_OK;
     case CSA_OP_SPARSE_ATTN_PAGED:
-      *bytes = paged_simt_ws_bytes(p, false, B, Tq, n_max);
+      *bytes = std::max(paged_simt_ws_bytes(p, false, B, Tq, n_max),
+                        attn_ws_bytes(p, CSA_BF16, false, B, Tq, n_max));
       return CSA_OK;
     case CSA_OP_HCA_ATTN_PAGED:
       *bytes = paged_simt_ws_bytes(p, true, B, Tq, n_max);
@@ -864,9 +865,9 @@ static csa_status_t launch_attn_simt(const AttnArgs& a, csa_dtype_t dtype, cudaS
   return launched("k_attn_simt");
 }
 
-template <bool kHca, bool kFp8 = false>
+template <bool kHca, bool kFp8 = false, bool kPaged = false>
 static csa_status_t launch_attn_tc(const csa_params_t* p, const AttnArgs& g, void* ws,
-                                   size_t ws_bytes, cudaStream_t s) {
+                                   size_t ws_bytes, cudaStream_t s, const PageMap& pm = PageMap{}) {
   const int LB = g.layers * g.B;  // (layer, sequence) rows of the grid
   const int sp = attn_splits(p, kHca, LB, g.Tq, g.n_max);
   const size_t need = attn_ws_bytes(p, CSA_BF16, kHca, LB, g.Tq, g.n_max);
@@ -914,7 +915,9 @@ static csa_status_t launch_attn_tc(const csa_params_t* p, const AttnArgs& g, voi
                            CU_TENSOR_MAP_SWIZZLE_64B));
   // row gathers (one-row boxes of 64 dims); a cache with no rows is never
   // read, and its map is made over q instead
-  const uint64_t n_cmp_rows = (uint64_t)g.B * g.n_max, n_raw_rows = (uint64_t)g.B * g.raw_max;
+  a.pm = pm;
+  const uint64_t n_cmp_rows = kPaged ? (uint64_t)pm.n_pages << pm.shift : (uint64_t)g.B * g.n_max;
+  const uint64_t n_raw_rows = (uint64_t)g.B * g.raw_max;
   const uint64_t n_q_rows = (uint64_t)g.B * g.Tq * kApHeads;
   if (kFp8) {  // E4M3 codes: one-row boxes of 128 dims (128 B)
     CSA_CHECK(make_tmap_u8(&tc, n_cmp_rows ? g.kv_cmp : g.q, kApDim,
@@ -927,9 +930,9 @@ static csa_status_t launch_attn_tc(const csa_params_t* p, const AttnArgs& g, voi
     CSA_CHECK(make_tmap_bf16(&tr, n_raw_rows ? g.kv_raw : g.q, kApDim,
                              n_raw_rows ? n_raw_rows : n_q_rows, 64, 1));
   }
-  CSA_CHECK(set_smem_attr(k_attn_pair<kHca, kFp8>, kApSmemBytes, "k_attn_pair"));
+  CSA_CHECK(set_smem_attr(k_attn_pair<kHca, kFp8, kPaged>, kApSmemBytes, "k_attn_pair"));
   dim3 grid((unsigned)(2 * sp), (unsigned)(LB * g.Tq));
-  cudaError_t e = launch_ex(k_attn_pair<kHca, kFp8>, grid,
+  cudaError_t e = launch_ex(k_attn_pair<kHca, kFp8, kPaged>, grid,
                             dim3(kFp8 ? kApThreadsFp8 : kApThreads), kApSmemBytes, s, 2, a, tq, to,
                             tc, tr);
   if (e != cudaSuccess) return cuda_fail(e, "k_attn_pair");
@@ -1531,6 +1534,8 @@ CSA_API csa_status_t csa_sparse_attn_paged(const csa_params_t* p, csa_dtype_t dt
   CSA_CHECK(check_device());
   AttnArgs a = make_attn_args(p, q, q_pos, kv_pages, idx, nullptr, table_width * page_size, kv_raw,
                               raw_pos0, n_raw, raw_max, sink, B, Tq, out);
+  if (attn_tc_ok(p, dtype, false, a.n_max))
+    return launch_attn_tc<false, false, true>(p, a, ws, ws_bytes, (cudaStream_t)stream, pm);
   return paged_attn_simt<false>(p, dtype, a, pm, ws, ws_bytes, (cudaStream_t)stream);
 }
 
