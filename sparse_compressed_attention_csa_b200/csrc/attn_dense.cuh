@@ -1,0 +1,842 @@
+// Step 4 over a paged cache of any length, on tensor cores: shared-KV
+// attention of new tokens (up to 128 heads a group, d = 512, bf16) over every
+// visible entry and the window's raw rows, split over the GPU and joined.
+//
+//   z_i = scale q.r_i,  o = sum_i e^z_i r_i / (e^sink + sum_i e^z_i)
+//
+// One pass over the rows with a running maximum and sum per head.  A row is
+// 1 KB and takes 4 * 128 * 512 operations: at this machine's copy bandwidth
+// and matrix rate both need 0.16 ns a row, so neither may wait for the other.
+//
+// The output of a token (128 heads x 512 dims in fp32) would fill TMEM, so
+// two CTAs share a range of rows, each with half of the output's dims:
+//
+//   S   = Q K^T           all 512 dims, in BOTH CTAs (M = 128 heads, N = 64)
+//   O_c += P V[:, D_c]    the CTA's own 256 dims (N = 256)
+//
+// Computing S twice costs half as much matrix work again, and the rows are
+// read twice from L2 (once from HBM), but the CTAs never wait for each other:
+// swapping partial logits, as the selected-entry kernel does, costs about
+// 1.2 us per 64 rows here, more than the second S.
+//
+// TMEM (512 columns): O [0,256) | S [256,384) two buffers | Q of the own dims
+// as bf16 pairs [384,512).  Q of the other dims stays in shared memory (64
+// KB, the A operand from there); P overwrites its S as bf16 pairs.  The rest
+// of shared memory is a ring of five slots of 32 KB: 64 rows x 256 dims, a
+// tile being two of them (the other half's dims first: they are released
+// after S, the own dims' after O).
+//
+// Warps: 0-3 softmax, one head per thread (= TMEM lane), lazy rescale (a
+// head's maximum moves only past 2^8); 4-7 fetch, one 64-dim quarter of each
+// slot: a whole tile by TMA, a box per page, a tile with fewer than 64 rows
+// (or a page outside the pool) row by row with zeros in the missing ones, so
+// that what lies behind the last row is never multiplied; 8 issues the MMAs;
+// 9 fetches Q's other half.
+//
+// Split: all tiles (64 rows; a token's window tiles, then its entries') form
+// one sequence.  With no more tokens than CTA pairs each pair takes part of
+// ONE token: the fewest tiles L per pair for which sum ceil(tiles / L) fits.
+// Where that leaves a pair more than kAdSegTiles tiles above the mean, and
+// with more tokens than pairs, the sequence is cut into equal ranges instead,
+// and a pair goes from token to token.  A token that one pair holds whole is
+// finished there; the others' parts (O / l in fp16 with a power-of-two scale
+// per head, m and l in fp32) are joined by k_attn_dense_join in their order.
+#pragma once
+#include "attn_pair.cuh"
+#include "common.cuh"
+#include "mxfp4.cuh"
+#include "sm100.cuh"
+
+namespace csa {
+
+constexpr int kAdTile = 64;
+constexpr int kAdSlots = 5;
+constexpr int kAdSlotBytes = 32768;    // 64 rows x 256 dims, or 128 heads x 128 dims of Q
+constexpr int kAdChunk = 8192;         // 64 rows x 64 dims
+constexpr int kAdQChunk = 16384;       // 128 heads x 64 dims
+constexpr int kAdThreads = 320;
+constexpr int kAdSegTiles = 3;         // what changing tokens costs a pair, in tiles
+constexpr int kAdMaxPairs = 128;       // units a one-token-per-pair plan may hold
+constexpr size_t kAdPartHalfs = 2 * (size_t)kApHeads * kApHalf;  // fp16 values of one part
+constexpr int kAdMl = 3 * kApHeads;    // m, l, scale per CTA of a part
+
+struct AttnDenseArgs {
+  const int* q_pos;
+  const __nv_bfloat16* kv;
+  PageMap pm;
+  const int* n_cmp;
+  int n_max;
+  const __nv_bfloat16* kv_raw;
+  const int* raw_pos0;
+  const int* n_raw;
+  int raw_max;
+  const float* sink;
+  int Tq, H, groups, units;  // unit: (token, group of 128 heads)
+  int window, width, stride, rope_dim;
+  int pairs, box_rows;
+  float scale_log2;
+  unsigned long long wait_ns;
+  __nv_bfloat16* out;
+  __half* part_o;  // [2 pairs][2 halves][32 units of 8 dims][128 heads][8]
+  float* part_ml;  // [2 pairs][2 halves][3][128]: m (log2), l, scale
+  // what to join: per unit (units <= pairs) its first and last pair, else per
+  // pair the unit that starts in it and goes on, and that unit's last pair; a
+  // unit that one pair holds has the same first and last (or unit -1)
+  int2* desc;
+  double freq[kApMaxRope / 2];
+};
+
+struct AdMisc {
+  float cs[kApMaxRope / 2], sn[kApMaxRope / 2];
+  uint64_t full[kAdSlots], empty[kAdSlots];
+  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t q_full, q_free, q_ready, o_free, mma_drain;
+  uint32_t tmem_base;
+  int abort_flag;
+  int u0, pre0, g0, g1;  // this pair's first unit, that unit's first tile, its range of tiles
+  int total;             // tiles of all units
+  int last;              // one token per pair: the last pair of the unit (else -1)
+  int tmp[40];
+  int tl[kAdMaxPairs];
+};
+
+constexpr int kAdQOff = kAdSlots * kAdSlotBytes;
+constexpr int kAdMiscOff = kAdQOff + 4 * kAdQChunk;
+constexpr size_t kAdSmemBytes = (size_t)kAdMiscOff + sizeof(AdMisc) + 1024;
+static_assert(kAdSmemBytes <= 232448, "shared memory budget");
+
+// What a unit reads.
+struct AdUnit {
+  int token, b, t;
+  int n_sel, n_win;
+  int raw_row;  // row of kv_raw of the first window row
+  int win_tiles, tiles;
+};
+
+__device__ __forceinline__ AdUnit ad_unit(const AttnDenseArgs& a, int u) {
+  AdUnit x;
+  x.token = u / a.groups;
+  x.b = x.token / a.Tq;
+  x.t = a.q_pos[x.token];
+  x.n_sel = max(0, min(n_visible(x.t, a.n_cmp[x.b], a.width, a.stride), a.n_max));
+  const int rp0 = a.raw_pos0[x.b];
+  const int lo = max(max(0, x.t - a.window + 1), rp0);
+  const int hi = min(x.t, rp0 + min(a.n_raw[x.b], a.raw_max) - 1);
+  x.n_win = a.window > 0 && hi >= lo ? hi - lo + 1 : 0;
+  x.raw_row = x.b * a.raw_max + (lo - rp0);
+  x.win_tiles = (x.n_win + kAdTile - 1) / kAdTile;
+  x.tiles = max(1, x.win_tiles + (x.n_sel + kAdTile - 1) / kAdTile);
+  return x;
+}
+
+__global__ void __launch_bounds__(kAdThreads, 1)
+    k_attn_dense(const __grid_constant__ AttnDenseArgs a, const __grid_constant__ CUtensorMap tm_q,
+                 const __grid_constant__ CUtensorMap tm_kv,
+                 const __grid_constant__ CUtensorMap tm_raw) {
+  using namespace sm100;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* q_smem = ring + kAdQOff;
+  AdMisc& sm = *reinterpret_cast<AdMisc*>(ring + kAdMiscOff);
+  const int part = blockIdx.x & 1, pair = blockIdx.x >> 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int dim0 = part * kApHalf, other0 = kApHalf - dim0;
+  const int rope0 = kApDim - a.rope_dim;
+  const uint64_t wait_ns = a.wait_ns;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kAdSlots; ++s) {
+      mbar_init(&sm.full[s], 4);  // the fetching warps
+      mbar_init(&sm.empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.p_full[i], 128);
+      mbar_init(&sm.pv_done[i], 1);
+    }
+    mbar_init(&sm.q_full, 1);
+    mbar_init(&sm.q_free, 1);
+    mbar_init(&sm.q_ready, 128);
+    mbar_init(&sm.o_free, 128);
+    mbar_init(&sm.mma_drain, 1);
+    sm.abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(&sm.tmem_base, 512);
+    tmem_relinquish();
+  }
+  griddep_wait();  // the predecessor's writes are visible
+  griddep_launch_dependents();
+
+  // ---- this pair's range of tiles
+  {
+    const int per = (a.units + kAdThreads - 1) / kAdThreads;  // units per thread
+    const int ua = min(a.units, (int)threadIdx.x * per), ub = min(a.units, ua + per);
+    int mine = 0;
+    for (int u = ua; u < ub; ++u) {
+      const int n = ad_unit(a, u).tiles;
+      mine += n;
+      if (a.units <= a.pairs) sm.tl[u] = n;
+    }
+    int total = 0;
+    const int inc = block_inclusive_scan(mine, sm.tmp, &total);
+    bool one = false;  // one token per pair
+    int L = 1;
+    if (a.units <= a.pairs) {
+      for (int tries = 0; tries < 2; ++tries) {
+        const int room = tries == 0 ? a.pairs - a.units / 2 : a.pairs - a.units + 1;
+        L = (total + room - 1) / room;
+        int need = 0;
+        for (int u = lane; u < a.units; u += 32) need += (sm.tl[u] + L - 1) / L;
+        if (__reduce_add_sync(0xffffffffu, need) <= a.pairs) break;
+      }
+      one = L <= total / a.pairs + kAdSegTiles;
+    }
+    if (threadIdx.x == 0) {
+      sm.total = total;
+      if (!one) sm.last = -1;
+    }
+    if (one) {
+      if (warp == 0) {
+        int at = 0, pre = 0, found = 0;
+        for (int u0 = 0; u0 < a.units; u0 += 32) {
+          const int u = u0 + lane;
+          const int tl = u < a.units ? sm.tl[u] : 0;
+          const int cnt = (tl + L - 1) / L;
+          int ci = cnt, ti = tl;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int c2 = __shfl_up_sync(0xffffffffu, ci, o), t2 = __shfl_up_sync(0xffffffffu, ti, o);
+            if (lane >= o) {
+              ci += c2;
+              ti += t2;
+            }
+          }
+          const int k = pair - (at + ci - cnt);
+          if (k >= 0 && k < cnt) {
+            const int base = pre + ti - tl;
+            sm.u0 = u;
+            sm.pre0 = base;
+            sm.g0 = base + (int)((long long)tl * k / cnt);
+            sm.g1 = base + (int)((long long)tl * (k + 1) / cnt);
+            sm.last = pair + cnt - 1 - k;
+            found = 1;
+          }
+          at += __shfl_sync(0xffffffffu, ci, 31);
+          pre += __shfl_sync(0xffffffffu, ti, 31);
+        }
+        if (!__any_sync(0xffffffffu, found) && lane == 0) sm.g0 = sm.g1 = sm.u0 = sm.pre0 = 0;
+      }
+    } else {
+      const int g0 = (int)((long long)total * pair / a.pairs);
+      const int g1 = (int)((long long)total * (pair + 1) / a.pairs);
+      if (threadIdx.x == 0 && g0 == g1) sm.g0 = sm.g1 = sm.u0 = sm.pre0 = 0;
+      if (g0 < g1 && g0 >= inc - mine && g0 < inc) {  // the thread whose units hold tile g0
+        int pre = inc - mine, u = ua;
+        for (; u < ub; ++u) {
+          const int n = ad_unit(a, u).tiles;
+          if (g0 < pre + n) break;
+          pre += n;
+        }
+        sm.u0 = u;
+        sm.pre0 = pre;
+        sm.g0 = g0;
+        sm.g1 = g1;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  const uint32_t t_o = tmem, t_s = tmem + 256, t_q = tmem + 384;
+  volatile int* abortp = &sm.abort_flag;
+  const int g1 = sm.g1;
+  int u = sm.u0, pre = sm.pre0, g = sm.g0;
+  bool ok = true;
+
+  if (warp < 4) {
+    // ======================= softmax warps
+    const int head = warp * 32 + lane;  // of the unit's group = TMEM lane
+    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+    int item = 0;  // ring items passed
+    int gt = 0;    // tiles done, over all segments
+    int seg = 0;
+    bool joined = false;
+    for (; g < g1 && ok; ++seg) {
+      const AdUnit x = ad_unit(a, u);
+      const int tb = g - pre, te = min(x.tiles, g1 - pre);
+      const bool first = tb == 0, whole = first && te == x.tiles;
+      // ---- RoPE table, then Q: the own dims to TMEM, the other dims in place
+      asm volatile("bar.sync 1, 128;" ::: "memory");  // the last segment's table is done with
+      if (head < a.rope_dim / 2) {
+        float c, s;
+        rope_cs_reduced(x.t, a.freq[head], &c, &s);
+        sm.cs[head] = c;
+        sm.sn[head] = s;
+      }
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      auto rotate = [&](uint32_t (&w)[32], int d0) {  // 64 dims from d0
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const int d = d0 + 2 * e;
+          if (d >= rope0) {
+            const int i = (d - rope0) >> 1;
+            const float2 f = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&w[e]));
+            w[e] = ap_bf16x2(f.x * sm.cs[i] - f.y * sm.sn[i], f.x * sm.sn[i] + f.y * sm.cs[i]);
+          }
+        }
+      };
+      auto load64 = [&](const uint8_t* blk, uint32_t (&w)[32]) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint4 v = *reinterpret_cast<const uint4*>(blk + ap_swz(head, k));
+          w[4 * k] = v.x;
+          w[4 * k + 1] = v.y;
+          w[4 * k + 2] = v.z;
+          w[4 * k + 3] = v.w;
+        }
+      };
+      if (seg > 0)  // every QK of the last segment has read Q
+        ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_free, (uint32_t)(seg - 1) & 1u, abortp, wait_ns));
+      tc_fence_after();
+#pragma unroll 1
+      for (int half = 0; half < 2 && ok; ++half) {
+        const int slot = (item + half) % kAdSlots;
+        ok = __all_sync(0xffffffffu, mbar_wait(&sm.full[slot], (uint32_t)((item + half) / kAdSlots) & 1u,
+                                               abortp, wait_ns));
+        if (!ok) break;
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          uint32_t w[32], r16[16];
+          load64(ring + slot * kAdSlotBytes + c * kAdQChunk, w);
+          const int d0 = dim0 + half * 128 + c * 64;
+          if (d0 + 64 > rope0) rotate(w, d0);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) r16[e] = w[e];
+          tmem_st16(t_q + lane_base + (uint32_t)(half * 64 + c * 32), r16);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) r16[e] = w[16 + e];
+          tmem_st16(t_q + lane_base + (uint32_t)(half * 64 + c * 32 + 16), r16);
+        }
+      }
+      if (ok && other0 + kApHalf > rope0 && a.rope_dim > 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_full, (uint32_t)seg & 1u, abortp, wait_ns));
+        if (ok) {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            const int d0 = other0 + c * 64;
+            if (d0 + 64 <= rope0) continue;
+            uint8_t* blk = q_smem + c * kAdQChunk;
+            uint32_t w[32];
+            load64(blk, w);
+            rotate(w, d0);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<uint4*>(blk + ap_swz(head, k)) =
+                  make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+          }
+        }
+      }
+      tmem_wait_st();
+      fence_proxy_async_shared();
+      tc_fence_before();
+      ok = ap_softmax_all(ok);  // all have read the Q slots
+      if (!ok) break;
+      if (threadIdx.x == 0) {
+        mbar_arrive(&sm.empty[item % kAdSlots]);
+        mbar_arrive(&sm.empty[(item + 1) % kAdSlots]);
+      }
+      mbar_arrive(&sm.q_ready);
+      item += 2 + 2 * (te - tb);
+
+      // ---- the tiles
+      float m_run = -INFINITY, l_run = 0.f;
+      const int gt0 = gt;
+      for (int i = tb; i < te; ++i, ++gt) {
+        const int sb = gt & 1;
+        // valid rows of the tile
+        const bool win = i < x.win_tiles;
+        const int cnt = win ? x.n_win - i * kAdTile : x.n_sel - (i - x.win_tiles) * kAdTile;
+        uint32_t v0 = 0xffffffffu, v1 = 0xffffffffu;
+        if (cnt < kAdTile || !win) {
+          const int j = (i - x.win_tiles) * kAdTile + lane;
+          const bool ok0 = lane < cnt && (win || page_row(a.pm, x.b, a.n_max, j) >= 0);
+          const bool ok1 = lane + 32 < cnt && (win || page_row(a.pm, x.b, a.n_max, j + 32) >= 0);
+          v0 = __ballot_sync(0xffffffffu, ok0);
+          v1 = __ballot_sync(0xffffffffu, ok1);
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[sb], (uint32_t)(gt >> 1) & 1u, abortp, wait_ns));
+        if (!ok) break;
+        tc_fence_after();
+        float z[64];
+        {
+          uint32_t ra[32], rb[32];
+          tmem_ld32(t_s + lane_base + (uint32_t)(sb * 64), ra);
+          tmem_ld32(t_s + lane_base + (uint32_t)(sb * 64 + 32), rb);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            z[e] = __uint_as_float(ra[e]) * a.scale_log2;
+            z[32 + e] = __uint_as_float(rb[e]) * a.scale_log2;
+          }
+        }
+        if ((v0 & v1) != 0xffffffffu) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            if (!((v0 >> e) & 1u)) z[e] = -INFINITY;
+            if (!((v1 >> e) & 1u)) z[32 + e] = -INFINITY;
+          }
+        }
+        float mx[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mx[k] = z[k];
+#pragma unroll
+        for (int e = 8; e < 64; ++e) mx[e & 7] = fmaxf(mx[e & 7], z[e]);
+        const float mt = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                               fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+        const bool move = mt > m_run + kApRescaleLog2 || m_run == -INFINITY;
+        const float m_new = move ? mt : m_run;
+        if (gt > gt0 && __any_sync(0xffffffffu, move && m_run != -INFINITY)) {
+          // O holds P V of earlier tiles: wait for the last one, then rescale
+          ok = __all_sync(0xffffffffu, mbar_wait(&sm.pv_done[(gt - 1) & 1], (uint32_t)((gt - 1) >> 1) & 1u,
+                                                 abortp, wait_ns));
+          if (!ok) break;
+          tc_fence_after();
+          const float alpha = (move && m_run != -INFINITY) ? exp2f(m_run - m_new) : 1.f;
+#pragma unroll 1
+          for (int cc = 0; cc < kApHalf; cc += 32) {
+            uint32_t r[32], w16[16];
+            tmem_ld32(t_o + lane_base + (uint32_t)cc, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w16[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
+            tmem_st16(t_o + lane_base + (uint32_t)cc, w16);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w16[e] = __float_as_uint(__uint_as_float(r[16 + e]) * alpha);
+            tmem_st16(t_o + lane_base + (uint32_t)cc + 16, w16);
+          }
+          l_run *= alpha;
+        }
+        m_run = m_new;
+        uint32_t pk[32];
+        float ps8[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) ps8[k] = 0.f;
+        const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          // P in bf16, the operand of the product; the sum takes the rounded values
+          const float p0 = ap_ex2(z[2 * e] + neg_m);
+          const float p1 = ap_ex2(z[2 * e + 1] + neg_m);
+          __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
+          const float2 back = __bfloat1622float2(pb);
+          ps8[e & 7] += back.x + back.y;
+          pk[e] = *reinterpret_cast<uint32_t*>(&pb);
+        }
+        l_run += ((ps8[0] + ps8[1]) + (ps8[2] + ps8[3])) + ((ps8[4] + ps8[5]) + (ps8[6] + ps8[7]));
+        uint32_t w16[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) w16[e] = pk[e];
+        tmem_st16(t_s + lane_base + (uint32_t)(sb * 64), w16);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) w16[e] = pk[16 + e];
+        tmem_st16(t_s + lane_base + (uint32_t)(sb * 64 + 16), w16);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&sm.p_full[sb]);
+      }
+      // ---- epilogue
+      if (ok)
+        ok = __all_sync(0xffffffffu, mbar_wait(&sm.pv_done[(gt - 1) & 1], (uint32_t)((gt - 1) >> 1) & 1u,
+                                               abortp, wait_ns));
+      ok = ap_softmax_all(ok);
+      if (!ok) break;
+      tc_fence_after();
+      const int h = (u % a.groups) * kApHeads + head;  // head of the token
+      const bool live = h < a.H;
+      if (whole) {
+        const float sink_l2 = live ? a.sink[h] * 1.4426950408889634f : 0.f;
+        const float mm = fmaxf(m_run, sink_l2);
+        const float wm = m_run == -INFINITY ? 0.f : exp2f(m_run - mm);
+        const float den = l_run * wm + (sink_l2 == -INFINITY ? 0.f : exp2f(sink_l2 - mm));
+        const float scl = den > 0.f || den != den ? wm / den : 0.f;
+        __nv_bfloat16* orow = a.out + ((size_t)x.token * a.H + (live ? h : 0)) * kApDim + dim0;
+#pragma unroll 1
+        for (int sl = 0; sl < 8; ++sl) {
+          uint32_t r[32];
+          tmem_ld32(t_o + lane_base + (uint32_t)(sl * 32), r);
+          tmem_wait_ld();
+          float o[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(r[e]) * scl;
+          const int d0 = dim0 + sl * 32;
+          if (d0 + 32 > rope0) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const int d = d0 + e;
+              if (d >= rope0) {  // inverse rotation at -t
+                const int ii = (d - rope0) >> 1;
+                const float x0 = o[e], x1 = o[e + 1];
+                o[e] = x0 * sm.cs[ii] + x1 * sm.sn[ii];
+                o[e + 1] = -x0 * sm.sn[ii] + x1 * sm.cs[ii];
+              }
+            }
+          }
+          if (live) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              *reinterpret_cast<uint4*>(orow + sl * 32 + 8 * k) = make_uint4(
+                  ap_bf16x2(o[8 * k], o[8 * k + 1]), ap_bf16x2(o[8 * k + 2], o[8 * k + 3]),
+                  ap_bf16x2(o[8 * k + 4], o[8 * k + 5]), ap_bf16x2(o[8 * k + 6], o[8 * k + 7]));
+          }
+        }
+      } else {
+        // a part: O / l times a power of two that puts the head's largest
+        // value in [2^14, 2^15), in fp16 (11 bits where the output keeps 8)
+        const size_t part_i = ((size_t)(2 * pair + (first ? 1 : 0)) * 2 + part);
+        const float inv_l = l_run > 0.f ? 1.f / l_run : (l_run != l_run ? l_run : 0.f);
+        float top = 0.f;
+#pragma unroll 1
+        for (int sl = 0; sl < 8; ++sl) {
+          uint32_t r[32];
+          tmem_ld32(t_o + lane_base + (uint32_t)(sl * 32), r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) top = fmaxf(top, fabsf(__uint_as_float(r[e]) * inv_l));
+        }
+        const int field = (int)(__float_as_uint(top) >> 23);
+        const int up = field == 0 || field == 255 ? 0 : max(-100, min(100, 127 + 14 - field));
+        const float scl = __uint_as_float((uint32_t)(127 + up) << 23);
+        float* pml = a.part_ml + part_i * kAdMl;
+        pml[head] = m_run;
+        pml[kApHeads + head] = l_run;
+        pml[2 * kApHeads + head] = __uint_as_float((uint32_t)(127 - up) << 23);
+        const float mul = inv_l * scl;
+        uint4* po = reinterpret_cast<uint4*>(a.part_o + part_i * (kAdPartHalfs / 2)) + head;
+#pragma unroll 1
+        for (int sl = 0; sl < 8; ++sl) {
+          uint32_t r[32];
+          tmem_ld32(t_o + lane_base + (uint32_t)(sl * 32), r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t hv[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __half2 v = __floats2half2_rn(__uint_as_float(r[8 * k + 2 * e]) * mul,
+                                                  __uint_as_float(r[8 * k + 2 * e + 1]) * mul);
+              hv[e] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+            po[(sl * 4 + k) * kApHeads] = make_uint4(hv[0], hv[1], hv[2], hv[3]);
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&sm.o_free);
+      // the join's work list: the pair that holds a unit's first tile writes it
+      if (first && part == 0 && threadIdx.x == 0) {
+        // the pair of the unit's last tile: the largest p with total p / pairs <= that tile
+        const int last = sm.last >= 0 ? sm.last
+                                      : (int)(((long long)(pre + x.tiles) * a.pairs - 1) / sm.total);
+        if (a.units <= a.pairs) {
+          a.desc[u] = make_int2(pair, last);
+        } else if (!whole) {
+          a.desc[pair] = make_int2(u, last);
+          joined = true;
+        }
+      }
+      g = pre + te;
+      pre += x.tiles;
+      ++u;
+    }
+    if (a.units > a.pairs && part == 0 && threadIdx.x == 0 && !joined) a.desc[pair] = make_int2(-1, -1);
+  } else if (warp < 8) {
+    // ======================= fetching warps: 64-dim quarter q of each slot
+    const int q = warp - 4;
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_kv);
+      tma_prefetch_desc(&tm_raw);
+    }
+    int item = 0;
+    auto claim = [&](int n) -> bool {
+      bool r = true;
+      if (lane == 0)
+        r = mbar_wait(&sm.empty[n % kAdSlots], ((uint32_t)(n / kAdSlots) & 1u) ^ 1u, abortp, wait_ns);
+      return __shfl_sync(0xffffffffu, r ? 1 : 0, 0) != 0;
+    };
+    const int subs = kAdTile / a.box_rows;
+    while (g < g1 && ok) {
+      const AdUnit x = ad_unit(a, u);
+      const int tb = g - pre, te = min(x.tiles, g1 - pre);
+      // Q's own dims: two slots of 128 heads x 128 dims
+      for (int half = 0; half < 2; ++half, ++item) {
+        ok = claim(item);
+        if (!ok) break;
+        const int slot = item % kAdSlots;
+        if (lane == 0) {
+          if (q < 2) {
+            mbar_arrive_expect_tx(&sm.full[slot], kAdQChunk);
+            tma_load_2d(ring + slot * kAdSlotBytes + q * kAdQChunk, &tm_q, &sm.full[slot],
+                        dim0 + half * 128 + q * 64, x.token * a.H + (u % a.groups) * kApHeads);
+          } else {
+            mbar_arrive(&sm.full[slot]);
+          }
+        }
+      }
+      for (int i = tb; i < te && ok; ++i) {
+        const bool win = i < x.win_tiles;
+        const int j0 = (i - x.win_tiles) * kAdTile;
+        const int cnt = win ? x.n_win - i * kAdTile : x.n_sel - j0;
+        // boxes of a whole tile, one lane each
+        long long box = -1;
+        bool whole = cnt >= kAdTile;
+        if (whole) {
+          if (win)
+            box = lane == 0 ? (long long)x.raw_row + (long long)i * kAdTile : -1;
+          else if (lane < subs)
+            box = page_row(a.pm, x.b, a.n_max, j0 + lane * a.box_rows);
+          whole = __popc(__ballot_sync(0xffffffffu, box >= 0)) == (win ? 1 : subs);
+        }
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half, ++item) {
+          ok = claim(item);
+          if (!ok) break;
+          const int slot = item % kAdSlots;
+          const int d0 = (half == 0 ? other0 : dim0) + q * 64;
+          uint8_t* dst = ring + slot * kAdSlotBytes + q * kAdChunk;
+          if (whole) {
+            if (lane == 0) mbar_arrive_expect_tx(&sm.full[slot], kAdChunk);
+            __syncwarp();
+            if (box >= 0)
+              tma_load_2d(dst + (win ? 0 : lane * a.box_rows * 128), win ? &tm_raw : &tm_kv,
+                          &sm.full[slot], d0, (int)box);
+          } else {
+            // row by row: lane l copies 16-byte unit l % 8 of rows 4k + l / 8
+            const int un = lane & 7;
+            const uint32_t base = smem_u32(dst);
+#pragma unroll 4
+            for (int k = 0; k < 16; ++k) {
+              const int r = 4 * k + (lane >> 3);
+              const __nv_bfloat16* src = nullptr;
+              if (r < cnt) {
+                if (win) {
+                  src = a.kv_raw + ((long long)x.raw_row + (long long)i * kAdTile + r) * kApDim;
+                } else {
+                  const long long row = page_row(a.pm, x.b, a.n_max, j0 + r);
+                  if (row >= 0) {
+                    src = a.kv + row * kApDim;
+                  } else if (half == 0 && q == 0 && un == 0) {
+                    report_error(CSA_ERR_DEVICE_BOUNDS);
+                  }
+                }
+              }
+              cp_async16(base + (uint32_t)(r * 128 + ((un ^ (r & 7)) << 4)),
+                         src != nullptr ? src + d0 + un * 8 : a.out, src != nullptr);
+            }
+            cp_async_wait_all();
+            fence_proxy_async_shared();  // read by the MMA (async proxy)
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.full[slot]);
+          }
+        }
+      }
+      g = pre + te;
+      pre += x.tiles;
+      ++u;
+    }
+    // every copy into shared memory lands before the CTA may exit (the last
+    // one asked of each slot; an earlier one was used before it)
+    __syncwarp();
+    if (lane == 0)
+      for (int n = max(0, item - kAdSlots); n < item; ++n)
+        mbar_drain(&sm.full[n % kAdSlots], (uint32_t)(n / kAdSlots) & 1u, kApDrainNs);
+  } else if (warp == 8) {
+    // ======================= MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t id_qk = idesc_bf16_f32(128, kAdTile);
+      constexpr uint32_t id_pv = idesc_bf16_f32(128, kApHalf, 0, 1);
+      const uint32_t qa = smem_u32(q_smem);
+      int item = 0, gt = 0;
+      for (int seg = 0; g < g1 && ok; ++seg) {
+        const AdUnit x = ad_unit(a, u);
+        const int n = min(x.tiles, g1 - pre) - (g - pre);
+        item += 2;  // Q's own dims
+        ok = mbar_wait(&sm.q_full, (uint32_t)seg & 1u, abortp, wait_ns) &&
+             mbar_wait(&sm.q_ready, (uint32_t)seg & 1u, abortp, wait_ns);
+        for (int i = 0; i <= n && ok; ++i) {
+          if (i < n) {  // S(i) = Q K^T
+            const uint32_t d = t_s + (uint32_t)(((gt + i) & 1) * 64);
+            const int s0 = (item + 2 * i) % kAdSlots, s1 = (item + 2 * i + 1) % kAdSlots;
+            ok = mbar_wait(&sm.full[s0], (uint32_t)((item + 2 * i) / kAdSlots) & 1u, abortp, wait_ns);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t b0 = sw128_desc(smem_u32(ring + s0 * kAdSlotBytes), 16, 1024);
+            const uint64_t a0 = sw128_desc(qa, 16, 1024);
+#pragma unroll
+            for (int ks = 0; ks < 16; ++ks)
+              mma_ss(d, a0 + (uint64_t)(((ks >> 2) * kAdQChunk + (ks & 3) * 32) >> 4),
+                     b0 + (uint64_t)(((ks >> 2) * kAdChunk + (ks & 3) * 32) >> 4), id_qk, ks != 0);
+            tc_commit(&sm.empty[s0]);
+            ok = mbar_wait(&sm.full[s1], (uint32_t)((item + 2 * i + 1) / kAdSlots) & 1u, abortp, wait_ns);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t b1 = sw128_desc(smem_u32(ring + s1 * kAdSlotBytes), 16, 1024);
+#pragma unroll
+            for (int ks = 0; ks < 16; ++ks)
+              mma_ts(d, t_q + (uint32_t)((ks >> 2) * 32 + (ks & 3) * 8),
+                     b1 + (uint64_t)(((ks >> 2) * kAdChunk + (ks & 3) * 32) >> 4), id_qk, 1u);
+            tc_commit(&sm.s_full[(gt + i) & 1]);
+            if (i == n - 1) tc_commit(&sm.q_free);
+          }
+          if (i > 0) {  // O += P(i - 1) V
+            const int j = gt + i - 1, sb = j & 1;
+            if (i == 1 && seg > 0) {  // the last segment's O has been read
+              ok = mbar_wait(&sm.o_free, (uint32_t)(seg - 1) & 1u, abortp, wait_ns);
+              if (!ok) break;
+            }
+            ok = mbar_wait(&sm.p_full[sb], (uint32_t)(j >> 1) & 1u, abortp, wait_ns);
+            if (!ok) break;
+            tc_fence_after();
+            const int s1 = (item + 2 * (i - 1) + 1) % kAdSlots;
+            const uint64_t v0 = sw128_desc(smem_u32(ring + s1 * kAdSlotBytes), kAdChunk, 1024);
+#pragma unroll
+            for (int ks = 0; ks < kAdTile / 16; ++ks)
+              mma_ts(t_o, t_s + (uint32_t)(sb * 64 + ks * 8), v0 + (uint64_t)((ks * 16 * 128) >> 4), id_pv,
+                     (i > 1 || ks > 0) ? 1u : 0u);
+            tc_commit(&sm.empty[s1]);
+            tc_commit(&sm.pv_done[sb]);
+          }
+        }
+        item += 2 * n;
+        gt += n;
+        g += n;
+        pre += x.tiles;
+        ++u;
+      }
+      // TMEM is freed only after every MMA issued here has landed
+      tc_commit(&sm.mma_drain);
+      mbar_drain(&sm.mma_drain, 0, kApDrainNs);
+    }
+  } else {
+    // ======================= warp 9: Q's other half
+    if (lane == 0) {
+      int seg = 0, sent = 0;
+      for (; g < g1 && ok; ++seg) {
+        const AdUnit x = ad_unit(a, u);
+        if (seg > 0) ok = mbar_wait(&sm.q_free, (uint32_t)(seg - 1) & 1u, abortp, wait_ns);
+        if (!ok) break;
+        mbar_arrive_expect_tx(&sm.q_full, 4 * kAdQChunk);
+        for (int c = 0; c < 4; ++c)
+          tma_load_2d(q_smem + c * kAdQChunk, &tm_q, &sm.q_full, other0 + c * 64,
+                      x.token * a.H + (u % a.groups) * kApHeads);
+        sent = seg + 1;
+        g = pre + min(x.tiles, g1 - pre);
+        pre += x.tiles;
+        ++u;
+      }
+      if (sent > 0) mbar_drain(&sm.q_full, (uint32_t)(sent - 1) & 1u, kApDrainNs);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the parts of a unit that more than one pair holds.  One CTA per (8
+// dims, unit): thread (head, k) takes every kAdJoin-th part; the kAdJoin sums
+// of a head are added in their order.
+//   M = max(sink, max m_s),  L = 2^(sink - M) + sum l_s 2^(m_s - M)
+//   o = sum (l_s 2^(m_s - M) / L) O_s
+constexpr int kAdJoin = 4;
+
+__global__ void __launch_bounds__(kApHeads * kAdJoin) k_attn_dense_join(const __grid_constant__ AttnDenseArgs a) {
+  __shared__ float sm_o[kAdJoin][8][kApHeads];
+  __shared__ float sm_m[kAdJoin][kApHeads], sm_l[kAdJoin][kApHeads];
+  __shared__ float cs[4], sn[4];
+  sm100::griddep_wait();
+  sm100::griddep_launch_dependents();
+  const int2 ds = a.desc[blockIdx.y];
+  const bool by_unit = a.units <= a.pairs;
+  const int unit = by_unit ? (int)blockIdx.y : ds.x;
+  const int pair0 = by_unit ? ds.x : (int)blockIdx.y;
+  // nothing to join (or a launch that gave up before it wrote the list)
+  if (unit < 0 || unit >= a.units || pair0 < 0 || ds.y <= pair0 || ds.y >= a.pairs) return;
+  const int n = ds.y - pair0 + 1;
+  const int half = blockIdx.x >> 5, u8 = blockIdx.x & 31;
+  const int d0 = half * kApHalf + u8 * 8;
+  const int head = threadIdx.x & (kApHeads - 1), k = threadIdx.x / kApHeads;
+  const int rope0 = kApDim - a.rope_dim;
+  const int token = unit / a.groups, h = (unit % a.groups) * kApHeads + head;
+  if (threadIdx.x < 4 && d0 + 8 > rope0) {
+    const int d = d0 + 2 * (int)threadIdx.x;
+    cs[threadIdx.x] = 1.f;
+    sn[threadIdx.x] = 0.f;
+    if (d >= rope0) rope_cs_reduced(a.q_pos[token], a.freq[(d - rope0) >> 1], &cs[threadIdx.x], &sn[threadIdx.x]);
+  }
+  auto part_of = [&](int s) { return ((size_t)(2 * (pair0 + s) + (s == 0 ? 1 : 0))) * 2 + half; };
+  float mk = -INFINITY;
+  for (int s = k; s < n; s += kAdJoin) mk = fmaxf(mk, __ldcg(a.part_ml + part_of(s) * kAdMl + head));
+  sm_m[k][head] = mk;
+  __syncthreads();
+  const bool live = h < a.H;
+  const float sink_l2 = live ? a.sink[h] * 1.4426950408889634f : 0.f;
+  float M = sink_l2;
+#pragma unroll
+  for (int i = 0; i < kAdJoin; ++i) M = fmaxf(M, sm_m[i][head]);
+  float L = 0.f, o[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) o[e] = 0.f;
+#pragma unroll 4
+  for (int s = k; s < n; s += kAdJoin) {
+    const size_t pi = part_of(s);
+    const float* ml = a.part_ml + pi * kAdMl + head;
+    const float m = __ldcg(ml), l = __ldcg(ml + kApHeads), sc = __ldcg(ml + 2 * kApHeads);
+    const uint4 v = __ldcg(reinterpret_cast<const uint4*>(a.part_o + pi * (kAdPartHalfs / 2)) + u8 * kApHeads + head);
+    const float w = m == -INFINITY ? 0.f : l * exp2f(m - M);
+    L += w;
+    const float ws = w * sc;
+    const uint32_t hv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = ap_f16x2_to_f32(hv[e]);
+      o[2 * e] = fmaf(f.x, ws, o[2 * e]);
+      o[2 * e + 1] = fmaf(f.y, ws, o[2 * e + 1]);
+    }
+  }
+  sm_l[k][head] = L;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sm_o[k][e][head] = o[e];
+  __syncthreads();
+  if (k != 0 || !live) return;
+  L = sink_l2 == -INFINITY ? 0.f : exp2f(sink_l2 - M);
+#pragma unroll
+  for (int i = 0; i < kAdJoin; ++i) L += sm_l[i][head];
+  const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < kAdJoin; ++i) t += sm_o[i][e][head];
+    o[e] = t * inv;
+  }
+  if (d0 + 8 > rope0) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float x0 = o[2 * e], x1 = o[2 * e + 1];  // inverse rotation at -t
+      o[2 * e] = x0 * cs[e] + x1 * sn[e];
+      o[2 * e + 1] = -x0 * sn[e] + x1 * cs[e];
+    }
+  }
+  *reinterpret_cast<uint4*>(a.out + ((size_t)token * a.H + h) * kApDim + d0) =
+      make_uint4(ap_bf16x2(o[0], o[1]), ap_bf16x2(o[2], o[3]), ap_bf16x2(o[4], o[5]), ap_bf16x2(o[6], o[7]));
+}
+
+}  // namespace csa

@@ -13,6 +13,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "attn_dense.cuh"
 #include "attn_paged_simt.cuh"
 #include "attn_pair.cuh"
 #include "attn_simt.cuh"
@@ -467,6 +468,34 @@ size_t paged_simt_ws_bytes(const csa_params_t* p, bool hca, int B, int Tq, int n
   return round_up((size_t)B * Tq * p->n_heads * sp * (p->d + 2) * sizeof(float), 256);
 }
 
+// Paged HCA on tensor cores: any head count (groups of 128), d = 512, bf16.
+bool attn_dense_ok(const csa_params_t* p, csa_dtype_t dtype) {
+  return dtype == CSA_BF16 && p->d == kApDim && p->rope_dim <= kApMaxRope;
+}
+
+// CTA pairs of the dense paged kernel: every SM takes one CTA; no more pairs
+// than there can be tiles.
+int attn_dense_pairs(const csa_params_t* p, int B, int Tq, int n_max) {
+  const long long units = (long long)B * Tq * ((p->n_heads + kApHeads - 1) / kApHeads);
+  const long long tiles = ((long long)n_max + kAdTile - 1) / kAdTile +
+                          ((long long)p->window + kAdTile - 1) / kAdTile;
+  return (int)std::max<long long>(1, std::min<long long>(std::min(num_sms() / 2, kAdMaxPairs),
+                                                         units * std::max<long long>(1, tiles)));
+}
+
+struct DenseWs {
+  size_t o, ml, desc, total;
+};
+DenseWs attn_dense_ws(const csa_params_t* p, int B, int Tq, int n_max) {
+  const size_t pairs = (size_t)attn_dense_pairs(p, B, Tq, n_max);
+  DenseWs w;
+  w.o = 0;
+  w.ml = w.o + 2 * pairs * kAdPartHalfs * sizeof(__half);
+  w.desc = w.ml + round_up(2 * pairs * 2 * kAdMl * sizeof(float), 256);
+  w.total = w.desc + round_up(pairs * sizeof(int2), 256);
+  return w;
+}
+
 // Limit of every bounded device-side wait (csa_set_wait_limit_ns).
 constexpr unsigned long long kDefaultWaitNs = 2000000000ull;
 std::atomic<unsigned long long> g_wait_ns{kDefaultWaitNs};
@@ -525,6 +554,7 @@ CSA_API csa_status_t csa_workspace_size(const csa_params_t* p, csa_op_t op, int3
       return CSA_OK;
     case CSA_OP_HCA_ATTN_PAGED:
       *bytes = paged_simt_ws_bytes(p, true, B, Tq, n_max);
+      if (attn_dense_ok(p, CSA_BF16)) *bytes = std::max(*bytes, attn_dense_ws(p, B, Tq, n_max).total);
       return CSA_OK;
   }
   return fail(CSA_ERR_INVALID_ARGUMENT, "bad op %d", (int)op);
@@ -1502,6 +1532,67 @@ static csa_status_t paged_attn_simt(const csa_params_t* p, csa_dtype_t dtype, co
   return fail(CSA_ERR_UNSUPPORTED_SHAPE, "d=%d", g.d);
 }
 
+static csa_status_t launch_attn_dense(const csa_params_t* p, const AttnArgs& g, const PageMap& pm,
+                                      void* ws, size_t ws_bytes, cudaStream_t s) {
+  const DenseWs w = attn_dense_ws(p, g.B, g.Tq, g.n_max);
+  if (ws_bytes < w.total)
+    return fail(CSA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes, need %zu", ws_bytes, w.total);
+  CSA_CHECK(check_ptr(ws, "ws"));
+  AttnDenseArgs a;
+  a.q_pos = g.q_pos;
+  a.kv = (const __nv_bfloat16*)g.kv_cmp;
+  a.pm = pm;
+  a.n_cmp = g.n_cmp;
+  a.n_max = g.n_max;
+  a.kv_raw = (const __nv_bfloat16*)g.kv_raw;
+  a.raw_pos0 = g.raw_pos0;
+  a.n_raw = g.n_raw;
+  a.raw_max = g.raw_max;
+  a.sink = g.sink;
+  a.Tq = g.Tq;
+  a.H = g.H;
+  a.groups = (g.H + kApHeads - 1) / kApHeads;
+  const long long units = (long long)g.B * g.Tq * a.groups;
+  const long long tiles = ((long long)g.n_max + kAdTile - 1) / kAdTile +
+                          ((long long)g.window + kAdTile - 1) / kAdTile + 1;
+  if (units * tiles > 2147483647LL || (long long)g.B * g.raw_max > 2147483647LL ||
+      (long long)g.B * g.Tq * g.H > 2147483647LL)
+    return fail(CSA_ERR_UNSUPPORTED_SHAPE, "%lld query rows of up to %lld tiles: at most 2^31 - 1 in all",
+                units, tiles);
+  a.units = (int)units;
+  a.window = g.window;
+  a.width = g.width;
+  a.stride = g.stride;
+  a.rope_dim = g.rope_dim;
+  a.pairs = attn_dense_pairs(p, g.B, g.Tq, g.n_max);
+  a.box_rows = pm.shift < 6 ? 1 << pm.shift : kAdTile;
+  a.scale_log2 = g.scale * 1.4426950408889634f;
+  a.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
+  a.out = (__nv_bfloat16*)g.out;
+  a.part_o = (__half*)((char*)ws + w.o);
+  a.part_ml = (float*)((char*)ws + w.ml);
+  a.desc = (int2*)((char*)ws + w.desc);
+  for (int i = 0; i < kApMaxRope / 2; ++i) a.freq[i] = i < g.rope_dim / 2 ? rope_freq(g.rope, i) : 0.0;
+  CUtensorMap tq, tkv, tr;
+  const uint64_t q_rows = (uint64_t)g.B * g.Tq * g.H;
+  CSA_CHECK(make_tmap_bf16(&tq, g.q, kApDim, q_rows, 64, kApHeads));
+  // a cache with no rows is never read, and its map is made over q instead
+  const uint64_t kv_rows = (uint64_t)pm.n_pages << pm.shift, raw_rows = (uint64_t)g.B * g.raw_max;
+  CSA_CHECK(make_tmap_bf16(&tkv, kv_rows ? g.kv_cmp : g.q, kApDim, kv_rows ? kv_rows : q_rows, 64,
+                           (uint32_t)a.box_rows));
+  CSA_CHECK(make_tmap_bf16(&tr, raw_rows ? g.kv_raw : g.q, kApDim, raw_rows ? raw_rows : q_rows, 64, kAdTile));
+  CSA_CHECK(set_smem_attr(k_attn_dense, kAdSmemBytes, "k_attn_dense"));
+  cudaError_t e = launch_ex(k_attn_dense, dim3((unsigned)(2 * a.pairs)), dim3(kAdThreads), kAdSmemBytes, s, 1,
+                            a, tq, tkv, tr);
+  if (e != cudaSuccess) return cuda_fail(e, "k_attn_dense");
+  CSA_CHECK(launched("k_attn_dense"));
+  if (a.pairs == 1) return CSA_OK;  // every token is whole
+  e = launch_ex(k_attn_dense_join, dim3(kApDim / 8, (unsigned)std::min(a.units, a.pairs)),
+                dim3(kApHeads * kAdJoin), 0, s, 1, a);
+  if (e != cudaSuccess) return cuda_fail(e, "k_attn_dense_join");
+  return launched("k_attn_dense_join");
+}
+
 static csa_status_t paged_attn_checks(const csa_params_t* p, csa_dtype_t dtype, const void* q,
                                       const int32_t* q_pos, const void* kv_pages, int32_t n_pages,
                                       int32_t page_size, const int32_t* page_table,
@@ -1554,6 +1645,7 @@ CSA_API csa_status_t hca_attn_paged(const csa_params_t* p, csa_dtype_t dtype, co
   CSA_CHECK(check_device());
   AttnArgs a = make_attn_args(p, q, q_pos, kv_pages, nullptr, n_cmp, table_width * page_size,
                               kv_raw, raw_pos0, n_raw, raw_max, sink, B, Tq, out);
+  if (attn_dense_ok(p, dtype)) return launch_attn_dense(p, a, pm, ws, ws_bytes, (cudaStream_t)stream);
   return paged_attn_simt<true>(p, dtype, a, pm, ws, ws_bytes, (cudaStream_t)stream);
 }
 
