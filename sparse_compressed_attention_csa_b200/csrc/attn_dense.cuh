@@ -140,7 +140,8 @@ __global__ void __launch_bounds__(kAdThreads, 1)
   uint8_t* q_smem = ring + kAdQOff;
   AdMisc& sm = *reinterpret_cast<AdMisc*>(ring + kAdMiscOff);
   const int part = blockIdx.x & 1, pair = blockIdx.x >> 1;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the warp index, known to be the same in all lanes
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int dim0 = part * kApHalf, other0 = kApHalf - dim0;
   const int rope0 = kApDim - a.rope_dim;
   const uint64_t wait_ns = a.wait_ns;
@@ -655,36 +656,42 @@ __global__ void __launch_bounds__(kAdThreads, 1)
       for (int n = max(0, item - kAdSlots); n < item; ++n)
         mbar_drain(&sm.full[n % kAdSlots], (uint32_t)(n / kAdSlots) & 1u, kApDrainNs);
   } else if (warp == 8) {
-    // ======================= MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t id_qk = idesc_bf16_f32(128, kAdTile);
-      constexpr uint32_t id_pv = idesc_bf16_f32(128, kApHalf, 0, 1);
-      const uint32_t qa = smem_u32(q_smem);
-      int item = 0, gt = 0;
-      for (int seg = 0; g < g1 && ok; ++seg) {
-        const AdUnit x = ad_unit(a, u);
-        const int n = min(x.tiles, g1 - pre) - (g - pre);
-        item += 2;  // Q's own dims
-        ok = mbar_wait(&sm.q_full, (uint32_t)seg & 1u, abortp, wait_ns) &&
-             mbar_wait(&sm.q_ready, (uint32_t)seg & 1u, abortp, wait_ns);
-        for (int i = 0; i <= n && ok; ++i) {
-          if (i < n) {  // S(i) = Q K^T
-            const uint32_t d = t_s + (uint32_t)(((gt + i) & 1) * 64);
-            const int s0 = (item + 2 * i) % kAdSlots, s1 = (item + 2 * i + 1) % kAdSlots;
-            ok = mbar_wait(&sm.full[s0], (uint32_t)((item + 2 * i) / kAdSlots) & 1u, abortp, wait_ns);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t b0 = sw128_desc(smem_u32(ring + s0 * kAdSlotBytes), 16, 1024);
-            const uint64_t a0 = sw128_desc(qa, 16, 1024);
+    // ======================= MMA issuer (the whole warp runs the loop, one
+    // elected lane issues)
+    constexpr uint32_t id_qk = idesc_bf16_f32(128, kAdTile);
+    constexpr uint32_t id_pv = idesc_bf16_f32(128, kApHalf, 0, 1);
+    const uint32_t ring_a = smem_u32(ring);
+    const uint64_t a0 = sw128_desc(ring_a + kAdQOff, 16, 1024);
+    auto wait = [&](uint64_t* bar, int phase) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)phase & 1u, abortp, wait_ns)) != 0;
+    };
+    int item = 0, gt = 0;
+    for (int seg = 0; g < g1 && ok; ++seg) {
+      const AdUnit x = ad_unit(a, u);
+      const int n = min(x.tiles, g1 - pre) - (g - pre);
+      item += 2;  // Q's own dims
+      ok = wait(&sm.q_full, seg) && wait(&sm.q_ready, seg);
+      for (int i = 0; i <= n && ok; ++i) {
+        if (i < n) {  // S(i) = Q K^T
+          const uint32_t d = t_s + (uint32_t)(((gt + i) & 1) * 64);
+          const int i0 = item + 2 * i, s0 = i0 % kAdSlots, s1 = (i0 + 1) % kAdSlots;
+          ok = wait(&sm.full[s0], i0 / kAdSlots);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t b0 = sw128_desc(ring_a + s0 * kAdSlotBytes, 16, 1024);
+          if (elect_one()) {
 #pragma unroll
             for (int ks = 0; ks < 16; ++ks)
               mma_ss(d, a0 + (uint64_t)(((ks >> 2) * kAdQChunk + (ks & 3) * 32) >> 4),
                      b0 + (uint64_t)(((ks >> 2) * kAdChunk + (ks & 3) * 32) >> 4), id_qk, ks != 0);
             tc_commit(&sm.empty[s0]);
-            ok = mbar_wait(&sm.full[s1], (uint32_t)((item + 2 * i + 1) / kAdSlots) & 1u, abortp, wait_ns);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t b1 = sw128_desc(smem_u32(ring + s1 * kAdSlotBytes), 16, 1024);
+          }
+          __syncwarp();
+          ok = wait(&sm.full[s1], (i0 + 1) / kAdSlots);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t b1 = sw128_desc(ring_a + s1 * kAdSlotBytes, 16, 1024);
+          if (elect_one()) {
 #pragma unroll
             for (int ks = 0; ks < 16; ++ks)
               mma_ts(d, t_q + (uint32_t)((ks >> 2) * 32 + (ks & 3) * 8),
@@ -692,17 +699,17 @@ __global__ void __launch_bounds__(kAdThreads, 1)
             tc_commit(&sm.s_full[(gt + i) & 1]);
             if (i == n - 1) tc_commit(&sm.q_free);
           }
-          if (i > 0) {  // O += P(i - 1) V
-            const int j = gt + i - 1, sb = j & 1;
-            if (i == 1 && seg > 0) {  // the last segment's O has been read
-              ok = mbar_wait(&sm.o_free, (uint32_t)(seg - 1) & 1u, abortp, wait_ns);
-              if (!ok) break;
-            }
-            ok = mbar_wait(&sm.p_full[sb], (uint32_t)(j >> 1) & 1u, abortp, wait_ns);
-            if (!ok) break;
-            tc_fence_after();
-            const int s1 = (item + 2 * (i - 1) + 1) % kAdSlots;
-            const uint64_t v0 = sw128_desc(smem_u32(ring + s1 * kAdSlotBytes), kAdChunk, 1024);
+          __syncwarp();
+        }
+        if (i > 0) {  // O += P(i - 1) V
+          const int j = gt + i - 1, sb = j & 1;
+          if (i == 1 && seg > 0) ok = wait(&sm.o_free, seg - 1);  // the last segment's O has been read
+          ok = ok && wait(&sm.p_full[sb], j >> 1);
+          if (!ok) break;
+          tc_fence_after();
+          const int s1 = (item + 2 * (i - 1) + 1) % kAdSlots;
+          const uint64_t v0 = sw128_desc(ring_a + s1 * kAdSlotBytes, kAdChunk, 1024);
+          if (elect_one()) {
 #pragma unroll
             for (int ks = 0; ks < kAdTile / 16; ++ks)
               mma_ts(t_o, t_s + (uint32_t)(sb * 64 + ks * 8), v0 + (uint64_t)((ks * 16 * 128) >> 4), id_pv,
@@ -710,17 +717,21 @@ __global__ void __launch_bounds__(kAdThreads, 1)
             tc_commit(&sm.empty[s1]);
             tc_commit(&sm.pv_done[sb]);
           }
+          __syncwarp();
         }
-        item += 2 * n;
-        gt += n;
-        g += n;
-        pre += x.tiles;
-        ++u;
       }
-      // TMEM is freed only after every MMA issued here has landed
+      item += 2 * n;
+      gt += n;
+      g += n;
+      pre += x.tiles;
+      ++u;
+    }
+    // TMEM is freed only after every MMA issued here has landed
+    if (elect_one()) {
       tc_commit(&sm.mma_drain);
       mbar_drain(&sm.mma_drain, 0, kApDrainNs);
     }
+    __syncwarp();
   } else {
     // ======================= warp 9: Q's other half
     if (lane == 0) {

@@ -536,6 +536,20 @@ __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// One lane of the (converged) warp.  MMAs issued under it from code that the
+// whole warp runs keep their descriptors in uniform registers: 32 clocks per
+// M = 128, N = 64 MMA with A in TMEM, where one lane of a divergent branch,
+// moving each descriptor there by itself, issues one per 46.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, e;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 __device__ __forceinline__ uint32_t elect_lane0() { return (threadIdx.x & 31u) == 0u; }
 
 }  // namespace sm100
