@@ -74,7 +74,8 @@ struct AttnDenseArgs {
   int Tq, H, groups, units;  // unit: (token, group of 128 heads)
   int window, width, stride, rope_dim;
   int pairs, box_rows;
-  float scale_log2;
+  float scale_log2;  // |scale| log2(e), above 0
+  uint32_t flip;     // sign bits that a negative scale turns in Q
   unsigned long long wait_ns;
   __nv_bfloat16* out;
   __half* part_o;  // [2 pairs][2 halves][32 units of 8 dims][128 heads][8]
@@ -301,12 +302,12 @@ __global__ void __launch_bounds__(kAdThreads, 1)
         }
       };
       if (seg > 0)  // every QK of the last segment has read Q
-        ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_free, (uint32_t)(seg - 1) & 1u, abortp, wait_ns));
+        ok = __all_sync(0xffffffffu, mbar_wait_fast(&sm.q_free, (uint32_t)(seg - 1) & 1u, abortp, wait_ns));
       tc_fence_after();
 #pragma unroll 1
       for (int half = 0; half < 2 && ok; ++half) {
         const int slot = (item + half) % kAdSlots;
-        ok = __all_sync(0xffffffffu, mbar_wait(&sm.full[slot], (uint32_t)((item + half) / kAdSlots) & 1u,
+        ok = __all_sync(0xffffffffu, mbar_wait_fast(&sm.full[slot], (uint32_t)((item + half) / kAdSlots) & 1u,
                                                abortp, wait_ns));
         if (!ok) break;
 #pragma unroll 1
@@ -316,6 +317,8 @@ __global__ void __launch_bounds__(kAdThreads, 1)
           const int d0 = dim0 + half * 128 + c * 64;
           if (d0 + 64 > rope0) rotate(w, d0);
 #pragma unroll
+          for (int e = 0; e < 32; ++e) w[e] ^= a.flip;
+#pragma unroll
           for (int e = 0; e < 16; ++e) r16[e] = w[e];
           tmem_st16(t_q + lane_base + (uint32_t)(half * 64 + c * 32), r16);
 #pragma unroll
@@ -323,17 +326,19 @@ __global__ void __launch_bounds__(kAdThreads, 1)
           tmem_st16(t_q + lane_base + (uint32_t)(half * 64 + c * 32 + 16), r16);
         }
       }
-      if (ok && other0 + kApHalf > rope0 && a.rope_dim > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_full, (uint32_t)seg & 1u, abortp, wait_ns));
+      if (ok && (a.flip != 0u || (other0 + kApHalf > rope0 && a.rope_dim > 0))) {
+        ok = __all_sync(0xffffffffu, mbar_wait_fast(&sm.q_full, (uint32_t)seg & 1u, abortp, wait_ns));
         if (ok) {
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             const int d0 = other0 + c * 64;
-            if (d0 + 64 <= rope0) continue;
+            if (d0 + 64 <= rope0 && a.flip == 0u) continue;
             uint8_t* blk = q_smem + c * kAdQChunk;
             uint32_t w[32];
             load64(blk, w);
-            rotate(w, d0);
+            if (d0 + 64 > rope0) rotate(w, d0);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) w[e] ^= a.flip;
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               *reinterpret_cast<uint4*>(blk + ap_swz(head, k)) =
@@ -356,23 +361,25 @@ __global__ void __launch_bounds__(kAdThreads, 1)
       // ---- the tiles
       float m_run = -INFINITY, l_run = 0.f;
       const int gt0 = gt;
+      // whether rows lane and lane + 32 of tile i count; looked up a tile
+      // ahead, so that the table's latency is not on the tiles' path
+      auto valid_rows = [&](int i, bool* r0, bool* r1) {
+        const bool win = i < x.win_tiles;
+        const int j = (i - x.win_tiles) * kAdTile + lane;
+        const int cnt = win ? x.n_win - i * kAdTile : x.n_sel - (i - x.win_tiles) * kAdTile;
+        *r0 = lane < cnt && (win || page_row(a.pm, x.b, a.n_max, j) >= 0);
+        *r1 = lane + 32 < cnt && (win || page_row(a.pm, x.b, a.n_max, j + 32) >= 0);
+      };
+      bool nr0, nr1;
+      valid_rows(tb, &nr0, &nr1);
       for (int i = tb; i < te; ++i, ++gt) {
         const int sb = gt & 1;
-        // valid rows of the tile
-        const bool win = i < x.win_tiles;
-        const int cnt = win ? x.n_win - i * kAdTile : x.n_sel - (i - x.win_tiles) * kAdTile;
-        uint32_t v0 = 0xffffffffu, v1 = 0xffffffffu;
-        if (cnt < kAdTile || !win) {
-          const int j = (i - x.win_tiles) * kAdTile + lane;
-          const bool ok0 = lane < cnt && (win || page_row(a.pm, x.b, a.n_max, j) >= 0);
-          const bool ok1 = lane + 32 < cnt && (win || page_row(a.pm, x.b, a.n_max, j + 32) >= 0);
-          v0 = __ballot_sync(0xffffffffu, ok0);
-          v1 = __ballot_sync(0xffffffffu, ok1);
-        }
-        ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[sb], (uint32_t)(gt >> 1) & 1u, abortp, wait_ns));
+        const uint32_t v0 = __ballot_sync(0xffffffffu, nr0), v1 = __ballot_sync(0xffffffffu, nr1);
+        if (i + 1 < te) valid_rows(i + 1, &nr0, &nr1);
+        ok = __all_sync(0xffffffffu, mbar_wait_fast(&sm.s_full[sb], (uint32_t)(gt >> 1) & 1u, abortp, wait_ns));
         if (!ok) break;
         tc_fence_after();
-        float z[64];
+        float z[64];  // q.k, not scaled
         {
           uint32_t ra[32], rb[32];
           tmem_ld32(t_s + lane_base + (uint32_t)(sb * 64), ra);
@@ -380,8 +387,8 @@ __global__ void __launch_bounds__(kAdThreads, 1)
           tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            z[e] = __uint_as_float(ra[e]) * a.scale_log2;
-            z[32 + e] = __uint_as_float(rb[e]) * a.scale_log2;
+            z[e] = __uint_as_float(ra[e]);
+            z[32 + e] = __uint_as_float(rb[e]);
           }
         }
         if ((v0 & v1) != 0xffffffffu) {
@@ -397,12 +404,12 @@ __global__ void __launch_bounds__(kAdThreads, 1)
 #pragma unroll
         for (int e = 8; e < 64; ++e) mx[e & 7] = fmaxf(mx[e & 7], z[e]);
         const float mt = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                               fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+                               fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * a.scale_log2;
         const bool move = mt > m_run + kApRescaleLog2 || m_run == -INFINITY;
         const float m_new = move ? mt : m_run;
         if (gt > gt0 && __any_sync(0xffffffffu, move && m_run != -INFINITY)) {
           // O holds P V of earlier tiles: wait for the last one, then rescale
-          ok = __all_sync(0xffffffffu, mbar_wait(&sm.pv_done[(gt - 1) & 1], (uint32_t)((gt - 1) >> 1) & 1u,
+          ok = __all_sync(0xffffffffu, mbar_wait_fast(&sm.pv_done[(gt - 1) & 1], (uint32_t)((gt - 1) >> 1) & 1u,
                                                  abortp, wait_ns));
           if (!ok) break;
           tc_fence_after();
@@ -429,13 +436,12 @@ __global__ void __launch_bounds__(kAdThreads, 1)
         const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
-          // P in bf16, the operand of the product; the sum takes the rounded values
-          const float p0 = ap_ex2(z[2 * e] + neg_m);
-          const float p1 = ap_ex2(z[2 * e + 1] + neg_m);
-          __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
-          const float2 back = __bfloat1622float2(pb);
-          ps8[e & 7] += back.x + back.y;
-          pk[e] = *reinterpret_cast<uint32_t*>(&pb);
+          // the sum in fp32; P in bf16, the operand of the product (2^-9 of
+          // each weight, where the output keeps as many bits)
+          const float p0 = ap_ex2(fmaf(z[2 * e], a.scale_log2, neg_m));
+          const float p1 = ap_ex2(fmaf(z[2 * e + 1], a.scale_log2, neg_m));
+          ps8[e & 7] += p0 + p1;
+          pk[e] = ap_bf16x2(p0, p1);
         }
         l_run += ((ps8[0] + ps8[1]) + (ps8[2] + ps8[3])) + ((ps8[4] + ps8[5]) + (ps8[6] + ps8[7]));
         uint32_t w16[16];
@@ -451,7 +457,7 @@ __global__ void __launch_bounds__(kAdThreads, 1)
       }
       // ---- epilogue
       if (ok)
-        ok = __all_sync(0xffffffffu, mbar_wait(&sm.pv_done[(gt - 1) & 1], (uint32_t)((gt - 1) >> 1) & 1u,
+        ok = __all_sync(0xffffffffu, mbar_wait_fast(&sm.pv_done[(gt - 1) & 1], (uint32_t)((gt - 1) >> 1) & 1u,
                                                abortp, wait_ns));
       ok = ap_softmax_all(ok);
       if (!ok) break;
@@ -566,7 +572,7 @@ __global__ void __launch_bounds__(kAdThreads, 1)
     auto claim = [&](int n) -> bool {
       bool r = true;
       if (lane == 0)
-        r = mbar_wait(&sm.empty[n % kAdSlots], ((uint32_t)(n / kAdSlots) & 1u) ^ 1u, abortp, wait_ns);
+        r = mbar_wait_fast(&sm.empty[n % kAdSlots], ((uint32_t)(n / kAdSlots) & 1u) ^ 1u, abortp, wait_ns);
       return __shfl_sync(0xffffffffu, r ? 1 : 0, 0) != 0;
     };
     const int subs = kAdTile / a.box_rows;
@@ -663,7 +669,7 @@ __global__ void __launch_bounds__(kAdThreads, 1)
     const uint32_t ring_a = smem_u32(ring);
     const uint64_t a0 = sw128_desc(ring_a + kAdQOff, 16, 1024);
     auto wait = [&](uint64_t* bar, int phase) {
-      return __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)phase & 1u, abortp, wait_ns)) != 0;
+      return __all_sync(0xffffffffu, mbar_wait_fast(bar, (uint32_t)phase & 1u, abortp, wait_ns)) != 0;
     };
     int item = 0, gt = 0;
     for (int seg = 0; g < g1 && ok; ++seg) {
@@ -738,7 +744,7 @@ __global__ void __launch_bounds__(kAdThreads, 1)
       int seg = 0, sent = 0;
       for (; g < g1 && ok; ++seg) {
         const AdUnit x = ad_unit(a, u);
-        if (seg > 0) ok = mbar_wait(&sm.q_free, (uint32_t)(seg - 1) & 1u, abortp, wait_ns);
+        if (seg > 0) ok = mbar_wait_fast(&sm.q_free, (uint32_t)(seg - 1) & 1u, abortp, wait_ns);
         if (!ok) break;
         mbar_arrive_expect_tx(&sm.q_full, 4 * kAdQChunk);
         for (int c = 0; c < 4; ++c)

@@ -1566,7 +1566,10 @@ static csa_status_t launch_attn_dense(const csa_params_t* p, const AttnArgs& g, 
   a.rope_dim = g.rope_dim;
   a.pairs = attn_dense_pairs(p, g.B, g.Tq, g.n_max);
   a.box_rows = pm.shift < 6 ? 1 << pm.shift : kAdTile;
-  a.scale_log2 = g.scale * 1.4426950408889634f;
+  // a masked logit is -inf times the scale, so the scale is kept above 0: a
+  // negative one turns Q's signs, 0 becomes the smallest number (weights of 1)
+  a.scale_log2 = std::max(std::fabs(g.scale) * 1.4426950408889634f, 1.4e-45f);
+  a.flip = g.scale < 0.f ? 0x80008000u : 0u;
   a.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
   a.out = (__nv_bfloat16*)g.out;
   a.part_o = (__half*)((char*)ws + w.o);

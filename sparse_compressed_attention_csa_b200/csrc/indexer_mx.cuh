@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, MINB)
           const int j = j0 + lane + 32 * c;
           kr[c] = j < it.nv ? page_row(a.pm, it.b, a.n_max, j) : -1;
         }
-        if (lane == 0) ok = mbar_wait(&sm.empty[s], ((uint32_t)(n / STAGES) & 1u) ^ 1u, abortp, wait_ns);
+        if (lane == 0) ok = mbar_wait_fast(&sm.empty[s], ((uint32_t)(n / STAGES) & 1u) ^ 1u, abortp, wait_ns);
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         if (!ok) break;
         const unsigned boxes = __ballot_sync(0xffffffffu, box >= 0);
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, MINB)
     for (int k = 0; ok && item(k, &it); ++k) {
       if (it.te <= it.tb) continue;
       const int qb = n & 1;
-      if (lane == 0) ok = mbar_wait(&sm.q_empty[qb], ((uint32_t)(n >> 1) & 1u) ^ 1u, abortp, wait_ns);
+      if (lane == 0) ok = mbar_wait_fast(&sm.q_empty[qb], ((uint32_t)(n >> 1) & 1u) ^ 1u, abortp, wait_ns);
       ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       if (!ok) break;
       const long long row0 = (long long)it.b * a.Tq + it.t0;  // query token
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, MINB)
       const int qb = n & 1;
       const int blocks = (it.nq + NT - 1) / NT;
       if (lane == 0) {
-        ok = mbar_wait(&sm.q_full[qb], (uint32_t)(n >> 1) & 1u, abortp, wait_ns);
+        ok = mbar_wait_fast(&sm.q_full[qb], (uint32_t)(n >> 1) & 1u, abortp, wait_ns);
         if (ok) {
           fence_proxy_async_shared();  // scales came by cp.async (generic proxy)
           tc_fence_after();
@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, MINB)
           const uint32_t q_addr = smem_u32(sm.q[qb]);
           for (int i = it.tb; i < it.te && ok; ++i, ++tile) {
             const int s = tile % STAGES;
-            ok = mbar_wait(&sm.full[s], (uint32_t)(tile / STAGES) & 1u, abortp, wait_ns);
+            ok = mbar_wait_fast(&sm.full[s], (uint32_t)(tile / STAGES) & 1u, abortp, wait_ns);
             if (!ok) break;
             fence_proxy_async_shared();
             tc_fence_after();
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, MINB)
             const uint32_t k_addr = smem_u32(sm.keys[s]);
             for (int nb = 0; nb < blocks; ++nb, ++step) {
               const int acc = step % kImBufs;
-              ok = mbar_wait(&sm.acc_empty[acc], ((uint32_t)(step / kImBufs) & 1u) ^ 1u, abortp, wait_ns);
+              ok = mbar_wait_fast(&sm.acc_empty[acc], ((uint32_t)(step / kImBufs) & 1u) ^ 1u, abortp, wait_ns);
               if (!ok) break;
               tc_fence_after();
               const uint32_t d = tmem + (uint32_t)(acc * N);
@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, MINB)
       if (it.te <= it.tb) continue;
       const int qb = n & 1;
       const int blocks = (it.nq + NT - 1) / NT;
-      ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_full[qb], (uint32_t)(n >> 1) & 1u, abortp, wait_ns));
+      ok = __all_sync(0xffffffffu, mbar_wait_fast(&sm.q_full[qb], (uint32_t)(n >> 1) & 1u, abortp, wait_ns));
       for (int i = it.tb; i < it.te && ok; ++i) {
         const int j = i * kImKeys + quarter * 32 + lane;
         bool in_pool = true;
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, MINB)
         }
         for (int nb = 0; nb < blocks; ++nb, ++step) {
           const int acc = step % kImBufs;
-          ok = __all_sync(0xffffffffu, mbar_wait(&sm.acc_full[acc], (uint32_t)(step / kImBufs) & 1u, abortp, wait_ns));
+          ok = __all_sync(0xffffffffu, mbar_wait_fast(&sm.acc_full[acc], (uint32_t)(step / kImBufs) & 1u, abortp, wait_ns));
           if (!ok) break;
           tc_fence_after();
           const int tok = nb * NT + g;

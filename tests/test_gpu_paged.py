@@ -162,6 +162,21 @@ def test_large_logits_and_sinks():
     csa_poll_device_error()
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.05, 0.3])
+def test_scales_of_any_sign(scale):
+    p, t, _ = _case("bf16", 128, 512, 64, [700, 70], 1, 64, 1, 1, 20, 77)
+    p = Params(window=20, width=1, stride=1, scale=scale)
+    out = host64(_hca(p, t))
+    f = lambda a: a.double().cpu().numpy()  # noqa: E731
+    for b in range(2):
+        n = int(t["n_cmp"][b])
+        want = oracle.hca_attn(f(t["q"][b]), t["q_pos"][b].cpu().numpy(),
+                               oracle.paged_rows(t["kv"].float().cpu().numpy(), t["table"][b].cpu().numpy(), n), n,
+                               f(t["raw"][b]), int(t["pos0"][b]), int(t["n_raw"][b]), t["sink"].cpu().numpy(),
+                               scale, 20, 1, 1, 64, 1e4)
+        assert_close(out[b], want, "bf16", f"scale {scale}")
+
+
 @pytest.mark.parametrize("H,d,dtype", [(128, 512, "bf16"), (3, 64, "f32")])
 def test_pages_outside_the_pool_are_reported_and_skipped(H, d, dtype):
     rope = 64 if d == 512 else 32
