@@ -767,93 +767,92 @@ __global__ void __launch_bounds__(kAdThreads, 1)
   }
 }
 
-// Joins the parts of a unit that more than one pair holds.  One CTA per (8
-// dims, unit): thread (head, k) takes every kAdJoin-th part; the kAdJoin sums
-// of a head are added in their order.
+// Joins the parts of a unit that more than one pair holds:
 //   M = max(sink, max m_s),  L = 2^(sink - M) + sum l_s 2^(m_s - M)
 //   o = sum (l_s 2^(m_s - M) / L) O_s
-constexpr int kAdJoin = 4;
+// One CTA of 128 threads per (16 dims, 32 heads, unit).  A warp holds 8 heads
+// x 4 lanes; lane k of a head takes every 4th part, all its loads at once and
+// the maximum as it goes, the four states are joined by shuffles in a fixed
+// order, and lane k finishes 4 of the 16 dims.  No shared memory, so that the
+// CTAs can be resident while the attention kernel ends (it leaves 1 KB).
+constexpr int kAdJoinDims = 16;
 
-__global__ void __launch_bounds__(kApHeads * kAdJoin) k_attn_dense_join(const __grid_constant__ AttnDenseArgs a) {
-  __shared__ float sm_o[kAdJoin][8][kApHeads];
-  __shared__ float sm_m[kAdJoin][kApHeads], sm_l[kAdJoin][kApHeads];
-  __shared__ float cs[4], sn[4];
+__global__ void __launch_bounds__(128) k_attn_dense_join(const __grid_constant__ AttnDenseArgs a) {
+  const int slab = blockIdx.x >> 2;  // 16 dims
+  const int lane = threadIdx.x & 31, k = lane >> 3;
+  const int head = (int)(blockIdx.x & 3) * 32 + (int)(threadIdx.x >> 5) * 8 + (lane & 7);
+  const int half = slab >> 4, u8 = (slab & 15) * 2;  // two units of 8 dims
+  const int d0 = half * kApHalf + u8 * 8;
+  const int rope0 = kApDim - a.rope_dim;
   sm100::griddep_wait();
   sm100::griddep_launch_dependents();
-  const int2 ds = a.desc[blockIdx.y];
+  const int2 ds = __ldcg(a.desc + blockIdx.y);
   const bool by_unit = a.units <= a.pairs;
   const int unit = by_unit ? (int)blockIdx.y : ds.x;
   const int pair0 = by_unit ? ds.x : (int)blockIdx.y;
   // nothing to join (or a launch that gave up before it wrote the list)
   if (unit < 0 || unit >= a.units || pair0 < 0 || ds.y <= pair0 || ds.y >= a.pairs) return;
   const int n = ds.y - pair0 + 1;
-  const int half = blockIdx.x >> 5, u8 = blockIdx.x & 31;
-  const int d0 = half * kApHalf + u8 * 8;
-  const int head = threadIdx.x & (kApHeads - 1), k = threadIdx.x / kApHeads;
-  const int rope0 = kApDim - a.rope_dim;
   const int token = unit / a.groups, h = (unit % a.groups) * kApHeads + head;
-  if (threadIdx.x < 4 && d0 + 8 > rope0) {
-    const int d = d0 + 2 * (int)threadIdx.x;
-    cs[threadIdx.x] = 1.f;
-    sn[threadIdx.x] = 0.f;
-    if (d >= rope0) rope_cs_reduced(a.q_pos[token], a.freq[(d - rope0) >> 1], &cs[threadIdx.x], &sn[threadIdx.x]);
-  }
-  auto part_of = [&](int s) { return ((size_t)(2 * (pair0 + s) + (s == 0 ? 1 : 0))) * 2 + half; };
-  float mk = -INFINITY;
-  for (int s = k; s < n; s += kAdJoin) mk = fmaxf(mk, __ldcg(a.part_ml + part_of(s) * kAdMl + head));
-  sm_m[k][head] = mk;
-  __syncthreads();
   const bool live = h < a.H;
   const float sink_l2 = live ? a.sink[h] * 1.4426950408889634f : 0.f;
-  float M = sink_l2;
+  const int t = a.q_pos[token];
+  float m = -INFINITY, L = 0.f, o[16];
 #pragma unroll
-  for (int i = 0; i < kAdJoin; ++i) M = fmaxf(M, sm_m[i][head]);
-  float L = 0.f, o[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) o[e] = 0.f;
-#pragma unroll 4
-  for (int s = k; s < n; s += kAdJoin) {
-    const size_t pi = part_of(s);
+  for (int e = 0; e < 16; ++e) o[e] = 0.f;
+#pragma unroll 2
+  for (int s = k; s < n; s += 4) {
+    const size_t pi = (size_t)(2 * (pair0 + s) + (s == 0 ? 1 : 0)) * 2 + half;
     const float* ml = a.part_ml + pi * kAdMl + head;
-    const float m = __ldcg(ml), l = __ldcg(ml + kApHeads), sc = __ldcg(ml + 2 * kApHeads);
-    const uint4 v = __ldcg(reinterpret_cast<const uint4*>(a.part_o + pi * (kAdPartHalfs / 2)) + u8 * kApHeads + head);
-    const float w = m == -INFINITY ? 0.f : l * exp2f(m - M);
-    L += w;
+    const uint4* po = reinterpret_cast<const uint4*>(a.part_o + pi * (kAdPartHalfs / 2)) + u8 * kApHeads + head;
+    const float ms = __ldcg(ml), ls = __ldcg(ml + kApHeads), sc = __ldcg(ml + 2 * kApHeads);
+    const uint4 v0 = __ldcg(po), v1 = __ldcg(po + kApHeads);
+    const float mn = fmaxf(m, ms);
+    const float old = m == -INFINITY ? 0.f : exp2f(m - mn);
+    const float w = ms == -INFINITY ? 0.f : ls * exp2f(ms - mn);
+    m = mn;
+    L = fmaf(L, old, w);
     const float ws = w * sc;
-    const uint32_t hv[4] = {v.x, v.y, v.z, v.w};
+    const uint32_t hv[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < 8; ++e) {
       const float2 f = ap_f16x2_to_f32(hv[e]);
-      o[2 * e] = fmaf(f.x, ws, o[2 * e]);
-      o[2 * e + 1] = fmaf(f.y, ws, o[2 * e + 1]);
+      o[2 * e] = fmaf(f.x, ws, o[2 * e] * old);
+      o[2 * e + 1] = fmaf(f.y, ws, o[2 * e + 1] * old);
     }
   }
-  sm_l[k][head] = L;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) sm_o[k][e][head] = o[e];
-  __syncthreads();
-  if (k != 0 || !live) return;
-  L = sink_l2 == -INFINITY ? 0.f : exp2f(sink_l2 - M);
-#pragma unroll
-  for (int i = 0; i < kAdJoin; ++i) L += sm_l[i][head];
+  // the four lanes of the head
+  float M = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+  M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
+  M = fmaxf(M, sink_l2);
+  const float f = m == -INFINITY ? 0.f : exp2f(m - M);
+  L *= f;
+  L += __shfl_xor_sync(0xffffffffu, L, 8);
+  L += __shfl_xor_sync(0xffffffffu, L, 16);
+  L += sink_l2 == -INFINITY ? 0.f : exp2f(sink_l2 - M);
   const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+  float y[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    float t = 0.f;
-#pragma unroll
-    for (int i = 0; i < kAdJoin; ++i) t += sm_o[i][e][head];
-    o[e] = t * inv;
+  for (int e = 0; e < 16; ++e) {
+    float v = o[e] * f;
+    v += __shfl_xor_sync(0xffffffffu, v, 8);
+    v += __shfl_xor_sync(0xffffffffu, v, 16);
+    if ((e >> 2) == k) y[e & 3] = v * inv;
   }
-  if (d0 + 8 > rope0) {
+  const int d = d0 + 4 * k;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float x0 = o[2 * e], x1 = o[2 * e + 1];  // inverse rotation at -t
-      o[2 * e] = x0 * cs[e] + x1 * sn[e];
-      o[2 * e + 1] = -x0 * sn[e] + x1 * cs[e];
+  for (int e = 0; e < 4; e += 2) {
+    if (d + e >= rope0) {  // inverse rotation at -t
+      float c, s;
+      rope_cs_reduced(t, a.freq[(d + e - rope0) >> 1], &c, &s);
+      const float x0 = y[e], x1 = y[e + 1];
+      y[e] = x0 * c + x1 * s;
+      y[e + 1] = -x0 * s + x1 * c;
     }
   }
-  *reinterpret_cast<uint4*>(a.out + ((size_t)token * a.H + h) * kApDim + d0) =
-      make_uint4(ap_bf16x2(o[0], o[1]), ap_bf16x2(o[2], o[3]), ap_bf16x2(o[4], o[5]), ap_bf16x2(o[6], o[7]));
+  if (live)
+    *reinterpret_cast<uint2*>(a.out + ((size_t)token * a.H + h) * kApDim + d) =
+        make_uint2(ap_bf16x2(y[0], y[1]), ap_bf16x2(y[2], y[3]));
 }
 
 }  // namespace csa

@@ -1159,9 +1159,9 @@ CSA_API csa_status_t hca_attn_fp8(const csa_params_t* p, const void* q, const in
 // The paged, 4-bit serving path: norm + RoPE of query and key heads, MXFP4
 // rows, the indexer's product on them, attention over paged caches.
 // ---------------------------------------------------------------------------
-template <typename T, int NV>
+template <typename T, int NV, int kRows>
 static cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t s) {
-  return launch_ex(k_norm_rope<T, NV>, dim3((unsigned)(a.side[0].blocks + a.side[1].blocks)),
+  return launch_ex(k_norm_rope<T, NV, kRows>, dim3((unsigned)(a.side[0].blocks + a.side[1].blocks)),
                    dim3(kNormThreads), 0, s, 1, a);
 }
 
@@ -1250,16 +1250,19 @@ CSA_API csa_status_t csa_norm_rope(const csa_params_t* p, csa_dtype_t dtype, int
   const RopeSpec rope = rope_spec(p);
   for (int i = 0; i < a.rope_dim / 2; ++i) a.freq[i] = rope_freq(rope, i);
   cudaStream_t s = (cudaStream_t)stream;
+  // heads at a time: two where a group has several, so that a warp keeps two
+  // rows in flight and their shuffles overlap
+  const bool two = a.side[0].hpg > 1 || a.side[1].hpg > 1;
   cudaError_t e;
   if (dtype == CSA_BF16)
-    e = nv == 1 ? launch_norm_rope<__nv_bfloat16, 1>(a, s)
-                : (nv == 2 ? launch_norm_rope<__nv_bfloat16, 2>(a, s)
-                           : launch_norm_rope<__nv_bfloat16, 4>(a, s));
+    e = nv == 1   ? (two ? launch_norm_rope<__nv_bfloat16, 1, 2>(a, s) : launch_norm_rope<__nv_bfloat16, 1, 1>(a, s))
+        : nv == 2 ? (two ? launch_norm_rope<__nv_bfloat16, 2, 2>(a, s) : launch_norm_rope<__nv_bfloat16, 2, 1>(a, s))
+                  : launch_norm_rope<__nv_bfloat16, 4, 1>(a, s);
   else
-    e = nv == 1   ? launch_norm_rope<float, 1>(a, s)
-        : nv == 2 ? launch_norm_rope<float, 2>(a, s)
-        : nv == 4 ? launch_norm_rope<float, 4>(a, s)
-                  : launch_norm_rope<float, 8>(a, s);
+    e = nv == 1   ? (two ? launch_norm_rope<float, 1, 2>(a, s) : launch_norm_rope<float, 1, 1>(a, s))
+        : nv == 2 ? launch_norm_rope<float, 2, 1>(a, s)
+        : nv == 4 ? launch_norm_rope<float, 4, 1>(a, s)
+                  : launch_norm_rope<float, 8, 1>(a, s);
   if (e != cudaSuccess) return cuda_fail(e, "k_norm_rope");
   return launched("k_norm_rope");
 }
@@ -1358,7 +1361,7 @@ static csa_status_t index_mx_checks(const csa_params_t* p, const uint8_t* q_code
   return check_ptr(n_cmp, "n_cmp");
 }
 
-template <int NT, int QU, int STAGES, int MINB>
+template <int NT, int QU, int STAGES, int PAR, int MINB>
 static csa_status_t launch_index_mx(const csa_params_t* p, const uint8_t* q_codes,
                                     const uint8_t* q_scales, const float* w,
                                     const uint8_t* k_codes, const uint8_t* k_scales,
@@ -1392,10 +1395,11 @@ static csa_status_t launch_index_mx(const csa_params_t* p, const uint8_t* q_code
   const uint64_t krows = pm.table != nullptr ? (uint64_t)pm.n_pages << pm.shift : (uint64_t)B * n_max;
   CSA_CHECK(make_tmap_mx(&tk, k_codes, krows, (uint32_t)a.box_rows));
   CSA_CHECK(make_tmap_mx(&tq, q_codes, (uint64_t)B * Tq * kImHeads, kImHeads));
-  auto kern = k_index_scores_mx<NT, QU, STAGES, MINB>;
+  auto kern = k_index_scores_mx<NT, QU, STAGES, PAR, MINB>;
   const size_t smem = sizeof(IdxMxSmem<NT, QU, STAGES>) + 1024;
   CSA_CHECK(set_smem_attr(kern, smem, "k_index_scores_mx"));
-  const cudaError_t e = launch_ex(kern, dim3((unsigned)grid), dim3(128 + 128 * NT), smem, s, 1, tk, tq, a);
+  const cudaError_t e = launch_ex(kern, dim3((unsigned)grid), dim3(128 + 128 * NT * PAR), smem, s,
+                                  1, tk, tq, a);
   if (e != cudaSuccess) return cuda_fail(e, "k_index_scores_mx");
   return launched("k_index_scores_mx");
 }
@@ -1411,9 +1415,9 @@ static csa_status_t index_mx_impl(const csa_params_t* p, const uint8_t* q_codes,
   const bool pool = pm.table == nullptr || pm.n_pages > 0;
   if (H_I == kImHeads && d_I == kImDim && pool) {
     if (Tq == 1)
-      return launch_index_mx<1, 1, 8, 2>(p, q_codes, q_scales, w, k_codes, k_scales, pm, q_pos, n_cmp,
+      return launch_index_mx<1, 1, 8, 1, 2>(p, q_codes, q_scales, w, k_codes, k_scales, pm, q_pos, n_cmp,
                                          B, Tq, n_max, scores, s);
-    return launch_index_mx<2, 16, 6, 1>(p, q_codes, q_scales, w, k_codes, k_scales, pm, q_pos, n_cmp,
+    return launch_index_mx<2, 16, 6, 2, 1>(p, q_codes, q_scales, w, k_codes, k_scales, pm, q_pos, n_cmp,
                                         B, Tq, n_max, scores, s);
   }
   dim3 grid((unsigned)(((long long)n_max + 127) / 128), (unsigned)Tq, (unsigned)B);
@@ -1590,8 +1594,8 @@ static csa_status_t launch_attn_dense(const csa_params_t* p, const AttnArgs& g, 
   if (e != cudaSuccess) return cuda_fail(e, "k_attn_dense");
   CSA_CHECK(launched("k_attn_dense"));
   if (a.pairs == 1) return CSA_OK;  // every token is whole
-  e = launch_ex(k_attn_dense_join, dim3(kApDim / 8, (unsigned)std::min(a.units, a.pairs)),
-                dim3(kApHeads * kAdJoin), 0, s, 1, a);
+  e = launch_ex(k_attn_dense_join, dim3(4 * kApDim / kAdJoinDims, (unsigned)std::min(a.units, a.pairs)),
+                dim3(128), 0, s, 1, a);
   if (e != cudaSuccess) return cuda_fail(e, "k_attn_dense_join");
   return launched("k_attn_dense_join");
 }

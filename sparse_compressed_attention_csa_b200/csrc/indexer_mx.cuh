@@ -17,8 +17,8 @@
 // l belongs to key l + 32 c), which also takes them through the page table.
 // Warp 1 (one thread) copies scales to TMEM and issues the MMAs into a ring
 // of three accumulators.  Warp 2 fetches a unit's queries, their scales and
-// the head weights, two units deep.  Warps 4.. read the accumulators back:
-// group g of four warps scores token g of the NT.
+// the head weights, two units deep.  Warps 4.. read the accumulators back, in
+// groups of four warps: one token of the NT, every PAR-th block.
 //
 // Work: a unit is up to QU query tokens of one sequence.  With no more units
 // than CTAs, the unit's key tiles are dealt to CTAs by a plan that every CTA
@@ -60,6 +60,7 @@ struct IdxMxSmem {
   uint32_t tmem_base;
   int abort_flag;
   int plan[3];  // this CTA's unit, first tile and end tile (planned launches)
+  int own[QU];  // entries visible to each of that unit's tokens
 };
 
 struct IdxMxArgs {
@@ -88,8 +89,8 @@ struct IdxMxTmem {
   static_assert(kUsed <= 512, "TMEM columns");
 };
 
-template <int NT, int QU, int STAGES, int MINB>
-__global__ void __launch_bounds__(128 + 128 * NT, MINB)
+template <int NT, int QU, int STAGES, int PAR, int MINB>
+__global__ void __launch_bounds__(128 + 128 * NT * PAR, MINB)
     k_index_scores_mx(const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_q,
                       const __grid_constant__ IdxMxArgs a) {
@@ -100,7 +101,8 @@ __global__ void __launch_bounds__(128 + 128 * NT, MINB)
   extern __shared__ uint8_t smem_raw[];
   S& sm = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                 ~static_cast<uintptr_t>(1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the warp index, known to be the same in all lanes
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint64_t wait_ns = a.wait_ns;
 
   if (threadIdx.x == 0) {
@@ -114,7 +116,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, MINB)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.q_full[i], 33);
-      mbar_init(&sm.q_empty[i], 4 * NT + 1);
+      mbar_init(&sm.q_empty[i], 4 * NT * PAR + 1);
     }
     mbar_init(&sm.mma_drain, 1);
     sm.abort_flag = 0;
@@ -190,6 +192,12 @@ __global__ void __launch_bounds__(128 + 128 * NT, MINB)
       sm.plan[1] = pb;
       sm.plan[2] = pe;
     }
+    __syncwarp();
+    const int u = sm.plan[0];
+    if (u >= 0 && lane < QU) {
+      const int b = u % a.B, t = u / a.B * QU + lane;
+      sm.own[lane] = t < a.Tq ? min(n_visible(a.q_pos[b * a.Tq + t], a.n_cmp[b], a.width, a.stride), a.n_max) : 0;
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -207,13 +215,26 @@ __global__ void __launch_bounds__(128 + 128 * NT, MINB)
       if (k > 0 || sm.plan[0] < 0) return false;
       it->u = sm.plan[0];
     } else {
-      const long long i = (long long)blockIdx.x + (long long)k * gridDim.x;
-      if (i >= a.units) return false;
+      // back and forth over the CTAs, so that their sums are near
+      const int c = (k & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x;
+      const long long i = (long long)c + (long long)k * gridDim.x;
+      if ((long long)k * gridDim.x >= a.units) return false;
       it->u = a.units - 1 - (int)i;
+      if (i >= a.units) it->u = -1;
+    }
+    if (it->u < 0) {  // no unit in this turn
+      it->tb = it->te = it->nv = it->nq = it->own = it->b = it->t0 = 0;
+      return true;
     }
     it->b = it->u % a.B;
     it->t0 = it->u / a.B * QU;
-    it->nv = unit_nv(it->u, &it->nq, &it->own);
+    if (a.planned) {
+      it->nq = min(QU, a.Tq - it->t0);
+      it->own = lane < QU ? sm.own[lane] : 0;
+      it->nv = __reduce_max_sync(0xffffffffu, it->own);
+    } else {
+      it->nv = unit_nv(it->u, &it->nq, &it->own);
+    }
     it->tb = a.planned ? sm.plan[1] : 0;
     it->te = a.planned ? sm.plan[2] : (it->nv + kImKeys - 1) / kImKeys;
     return true;
@@ -227,31 +248,39 @@ __global__ void __launch_bounds__(128 + 128 * NT, MINB)
     int n = 0;                              // tiles requested
     bool ok = true;
     for (int k = 0; ok && item(k, &it); ++k) {
-      for (int i = it.tb; i < it.te; ++i, ++n) {
-        const int s = n % STAGES;
-        // the pages' rows, looked up while the slot drains
+      // the rows of a tile's pages, looked up a tile ahead: box `lane` and
+      // keys lane + 32 c
+      struct Rows {
+        long long box, kr[4];
+      };
+      auto rows = [&](int i, Rows* r) {
         const int j0 = i * kImKeys;
         const int jb = j0 + lane * a.box_rows;
-        const long long box = lane < subs && jb < it.nv ? page_row(a.pm, it.b, a.n_max, jb) : -1;
-        long long kr[4];
+        r->box = lane < subs && jb < it.nv ? page_row(a.pm, it.b, a.n_max, jb) : -1;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int j = j0 + lane + 32 * c;
-          kr[c] = j < it.nv ? page_row(a.pm, it.b, a.n_max, j) : -1;
+          r->kr[c] = j < it.nv ? page_row(a.pm, it.b, a.n_max, j) : -1;
         }
-        if (lane == 0) ok = mbar_wait_fast(&sm.empty[s], ((uint32_t)(n / STAGES) & 1u) ^ 1u, abortp, wait_ns);
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      };
+      Rows cur, nxt;
+      if (it.tb < it.te) rows(it.tb, &nxt);
+      for (int i = it.tb; i < it.te; ++i, ++n) {
+        const int s = n % STAGES;
+        cur = nxt;
+        if (i + 1 < it.te) rows(i + 1, &nxt);
+        ok = __all_sync(0xffffffffu, mbar_wait_fast(&sm.empty[s], ((uint32_t)(n / STAGES) & 1u) ^ 1u, abortp, wait_ns));
         if (!ok) break;
-        const unsigned boxes = __ballot_sync(0xffffffffu, box >= 0);
+        const unsigned boxes = __ballot_sync(0xffffffffu, cur.box >= 0);
         if (lane == 0)
           mbar_arrive_expect_tx(&sm.full[s], (uint32_t)__popc(boxes) * (uint32_t)(a.box_rows * kImRow));
         __syncwarp();
-        if (box >= 0)
-          tma_load_2d(sm.keys[s] + lane * a.box_rows * kImRow, &tm_k, &sm.full[s], 0, (int)box);
+        if (cur.box >= 0)
+          tma_load_2d(sm.keys[s] + lane * a.box_rows * kImRow, &tm_k, &sm.full[s], 0, (int)cur.box);
         const uint32_t dst = smem_u32(sm.ks[s]) + (uint32_t)lane * 16u;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          cp_async4(dst + 4u * c, kr[c] >= 0 ? a.k_scales + kr[c] * kImScales : a.k_scales, kr[c] >= 0);
+          cp_async4(dst + 4u * c, cur.kr[c] >= 0 ? a.k_scales + cur.kr[c] * kImScales : a.k_scales, cur.kr[c] >= 0);
         cp_async_arrive(&sm.full[s]);
       }
     }
@@ -296,60 +325,74 @@ __global__ void __launch_bounds__(128 + 128 * NT, MINB)
       for (int i = max(0, n - 2); i < n; ++i)
         mbar_drain(&sm.q_full[i & 1], (uint32_t)(i >> 1) & 1u, kImDrainNs);
   } else if (warp == 1) {
-    // ---------------- MMA issuer
+    // ---------------- MMA issuer (the whole warp runs the loop, one elected
+    // lane issues)
     constexpr uint32_t id0 = idesc_mxf4(128, N, 0), id1 = idesc_mxf4(128, N, 2);
+    auto wait = [&](uint64_t* bar, uint32_t phase) {
+      return __all_sync(0xffffffffu, mbar_wait_fast(bar, phase & 1u, abortp, wait_ns)) != 0;
+    };
+    const uint32_t q0 = smem_u32(sm.q[0]), k0 = smem_u32(sm.keys[0]);
+    const uint32_t qs0 = smem_u32(sm.qs[0]), ks0 = smem_u32(sm.ks[0]);
     int n = 0, tile = 0, step = 0;
     bool ok = true;
     for (int k = 0; ok && item(k, &it); ++k) {
       if (it.te <= it.tb) continue;
       const int qb = n & 1;
       const int blocks = (it.nq + NT - 1) / NT;
-      if (lane == 0) {
-        ok = mbar_wait_fast(&sm.q_full[qb], (uint32_t)(n >> 1) & 1u, abortp, wait_ns);
-        if (ok) {
-          fence_proxy_async_shared();  // scales came by cp.async (generic proxy)
+      ok = wait(&sm.q_full[qb], (uint32_t)(n >> 1));
+      if (!ok) break;
+      fence_proxy_async_shared();  // scales came by cp.async (generic proxy)
+      tc_fence_after();
+      const uint32_t qs = qs0 + (uint32_t)qb * (S::kGroups * 512);
+      if (elect_one())
+        for (int g = 0; g < (it.nq * kImHeads + 127) / 128; ++g)
+          tc_cp_scales(t_sfb + (uint32_t)(qb * T::kSfb + 4 * g), scale_desc(qs + 512u * g));
+      __syncwarp();
+      const uint32_t q_addr = q0 + (uint32_t)qb * (QU * kImHeads * kImRow);
+      for (int i = it.tb; i < it.te && ok; ++i, ++tile) {
+        const int s = tile % STAGES;
+        ok = wait(&sm.full[s], (uint32_t)(tile / STAGES));
+        if (!ok) break;
+        fence_proxy_async_shared();
+        tc_fence_after();
+        // the buffer's last reader, tile - 4, has finished: at least four
+        // steps lie between, and the accumulators have three buffers
+        const uint32_t sfa = t_sfa + (uint32_t)((tile % kImSfa) * 4);
+        if (elect_one()) tc_cp_scales(sfa, scale_desc(ks0 + 512u * s));
+        __syncwarp();
+        const uint64_t ka = sw64_desc(k0 + (uint32_t)(s * kImKeys * kImRow), 512);
+        for (int nb = 0; nb < blocks; ++nb, ++step) {
+          const int acc = step % kImBufs;
+          ok = wait(&sm.acc_empty[acc], (uint32_t)(step / kImBufs) ^ 1u);
+          if (!ok) break;
           tc_fence_after();
-          for (int g = 0; g < (it.nq * kImHeads + 127) / 128; ++g)
-            tc_cp_scales(t_sfb + (uint32_t)(qb * T::kSfb + 4 * g), scale_desc(smem_u32(sm.qs[qb]) + 512u * g));
-          const uint32_t q_addr = smem_u32(sm.q[qb]);
-          for (int i = it.tb; i < it.te && ok; ++i, ++tile) {
-            const int s = tile % STAGES;
-            ok = mbar_wait_fast(&sm.full[s], (uint32_t)(tile / STAGES) & 1u, abortp, wait_ns);
-            if (!ok) break;
-            fence_proxy_async_shared();
-            tc_fence_after();
-            // the buffer's last reader, tile - 4, has finished: at least four
-            // steps lie between, and the accumulators have three buffers
-            const uint32_t sfa = t_sfa + (uint32_t)((tile % kImSfa) * 4);
-            tc_cp_scales(sfa, scale_desc(smem_u32(sm.ks[s])));
-            const uint32_t k_addr = smem_u32(sm.keys[s]);
-            for (int nb = 0; nb < blocks; ++nb, ++step) {
-              const int acc = step % kImBufs;
-              ok = mbar_wait_fast(&sm.acc_empty[acc], ((uint32_t)(step / kImBufs) & 1u) ^ 1u, abortp, wait_ns);
-              if (!ok) break;
-              tc_fence_after();
-              const uint32_t d = tmem + (uint32_t)(acc * N);
-              const uint32_t sfb = t_sfb + (uint32_t)(qb * T::kSfb + nb * (N / 32));
-              const uint32_t qa = q_addr + (uint32_t)(nb * N * kImRow);
-              mma_mxf4(d, sw64_desc(k_addr, 512), sw64_desc(qa, 512), id0, sfa, sfb, 0u);
-              mma_mxf4(d, sw64_desc(k_addr + 32, 512), sw64_desc(qa + 32, 512), id1, sfa, sfb, 1u);
-              tc_commit(&sm.acc_full[acc]);
+          const uint32_t d = tmem + (uint32_t)(acc * N);
+          const uint32_t sfb = t_sfb + (uint32_t)(qb * T::kSfb + nb * (N / 32));
+          const uint64_t qa = sw64_desc(q_addr + (uint32_t)(nb * N * kImRow), 512);
+          if (elect_one()) {
+            mma_mxf4(d, ka, qa, id0, sfa, sfb, 0u);
+            mma_mxf4(d, ka + 2, qa + 2, id1, sfa, sfb, 1u);  // 32 bytes on
+            tc_commit(&sm.acc_full[acc]);
+            if (nb == blocks - 1) {
+              tc_commit(&sm.empty[s]);
+              if (i == it.te - 1) tc_commit(&sm.q_empty[qb]);
             }
-            if (ok) tc_commit(&sm.empty[s]);
           }
-          if (ok) tc_commit(&sm.q_empty[qb]);
+          __syncwarp();
         }
       }
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       ++n;
     }
-    if (lane == 0) {  // TMEM is freed only after every MMA and copy has landed
+    if (elect_one()) {  // TMEM is freed only after every MMA and copy has landed
       tc_commit(&sm.mma_drain);
       mbar_drain(&sm.mma_drain, 0, kImDrainNs);
     }
+    __syncwarp();
   } else if (warp >= 4) {
-    // ---------------- epilogue: group g takes token g of each block
+    // ---------------- epilogue: group g takes token g % NT of every PAR-th
+    // block (step % PAR = g / NT)
     const int g = (warp - 4) >> 2, quarter = warp & 3;
+    const int tk = g % NT, par = g / NT;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     int n = 0, step = 0;
     bool ok = true;
@@ -366,48 +409,43 @@ __global__ void __launch_bounds__(128 + 128 * NT, MINB)
           if (!in_pool && g == 0) report_error(CSA_ERR_DEVICE_BOUNDS);
         }
         for (int nb = 0; nb < blocks; ++nb, ++step) {
+          if (PAR > 1 && step % PAR != par) continue;
           const int acc = step % kImBufs;
           ok = __all_sync(0xffffffffu, mbar_wait_fast(&sm.acc_full[acc], (uint32_t)(step / kImBufs) & 1u, abortp, wait_ns));
           if (!ok) break;
           tc_fence_after();
-          const int tok = nb * NT + g;
+          const int tok = nb * NT + tk;
           const int nv = __shfl_sync(0xffffffffu, it.own, tok & 31);  // 0 past nq
+          float s[4] = {0.f, 0.f, 0.f, 0.f};
           if (tok < it.nq) {
-            uint32_t r0[32], r1[32];
-            const uint32_t col = tmem + lane_base + (uint32_t)(acc * N + g * kImHeads);
-            tmem_ld32(col, r0);
-            tmem_ld32(col + 32, r1);
-            tmem_wait_ld();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.acc_empty[acc]);
+            const uint32_t col = tmem + lane_base + (uint32_t)(acc * N + tk * kImHeads);
             // four sums, joined at the end; a NaN passes through the maximum
             const float4* w = reinterpret_cast<const float4*>(sm.w[qb][tok]);
-            float s[4] = {0.f, 0.f, 0.f, 0.f};
             auto relu = [](uint32_t x) {
               float y;
               asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(__uint_as_float(x)));
               return y;
             };
 #pragma unroll
-            for (int h = 0; h < 8; ++h) {
-              const float4 wa = w[h], wb = w[8 + h];
-              s[0] = fmaf(wa.x, relu(r0[4 * h]), s[0]);
-              s[1] = fmaf(wa.y, relu(r0[4 * h + 1]), s[1]);
-              s[2] = fmaf(wa.z, relu(r0[4 * h + 2]), s[2]);
-              s[3] = fmaf(wa.w, relu(r0[4 * h + 3]), s[3]);
-              s[0] = fmaf(wb.x, relu(r1[4 * h]), s[0]);
-              s[1] = fmaf(wb.y, relu(r1[4 * h + 1]), s[1]);
-              s[2] = fmaf(wb.z, relu(r1[4 * h + 2]), s[2]);
-              s[3] = fmaf(wb.w, relu(r1[4 * h + 3]), s[3]);
+            for (int half = 0; half < 2; ++half) {
+              uint32_t r[32];
+              tmem_ld32(col + (uint32_t)(half * 32), r);
+              tmem_wait_ld();
+#pragma unroll
+              for (int h = 0; h < 8; ++h) {
+                const float4 wh = w[half * 8 + h];
+                s[0] = fmaf(wh.x, relu(r[4 * h]), s[0]);
+                s[1] = fmaf(wh.y, relu(r[4 * h + 1]), s[1]);
+                s[2] = fmaf(wh.z, relu(r[4 * h + 2]), s[2]);
+                s[3] = fmaf(wh.w, relu(r[4 * h + 3]), s[3]);
+              }
             }
-            if (j < nv && in_pool)
-              a.scores[((long long)it.b * a.Tq + it.t0 + tok) * a.n_max + j] = (s[0] + s[1]) + (s[2] + s[3]);
-          } else {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.acc_empty[acc]);
           }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.acc_empty[acc]);
+          if (j < nv && in_pool)
+            a.scores[((long long)it.b * a.Tq + it.t0 + tok) * a.n_max + j] = (s[0] + s[1]) + (s[2] + s[3]);
         }
       }
       __syncwarp();

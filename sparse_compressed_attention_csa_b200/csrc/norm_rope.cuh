@@ -58,7 +58,22 @@ __device__ __forceinline__ void norm_cos_sin(long long pos, double freq, float* 
   *c = fmaf(-sh, lo, ch);
 }
 
-template <typename T, int NV>
+__device__ __forceinline__ void norm_values(uint4 u, float (&v)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    v[2 * k] = __uint_as_float(w[k] << 16);
+    v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void norm_values(uint4 u, float (&v)[4]) {
+  v[0] = __uint_as_float(u.x);
+  v[1] = __uint_as_float(u.y);
+  v[2] = __uint_as_float(u.z);
+  v[3] = __uint_as_float(u.w);
+}
+
+template <typename T, int NV, int kRows>
 __global__ void __launch_bounds__(kNormThreads) k_norm_rope(const __grid_constant__ NormRopeArgs a) {
   constexpr int VEC = 16 / (int)sizeof(T);
   sm100::griddep_wait();
@@ -88,15 +103,20 @@ __global__ void __launch_bounds__(kNormThreads) k_norm_rope(const __grid_constan
   const T* src = static_cast<const T*>(sd.x) + (long long)row * sd.row_stride + (long long)h0 * dim;
   T* dst = static_cast<T*>(sd.out) + (orow * sd.heads + h0) * (long long)dim;
 
-  // the first head's values are in flight while the table is formed
-  float v[NV][VEC];
+  // kRows heads at a time, the next ones' values in flight as loaded
+  uint4 nx[kRows][NV];
+  auto fetch = [&](int h) {
 #pragma unroll
-  for (int n = 0; n < NV; ++n) {
-    const int c0 = (lane + n * G) * VEC;
+    for (int r = 0; r < kRows; ++r)
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) v[n][k] = 0.f;
-    if (nh > 0 && c0 < dim) load16(src + c0, v[n]);
-  }
+      for (int n = 0; n < NV; ++n) {
+        const int c0 = (lane + n * G) * VEC;
+        nx[r][n] = make_uint4(0u, 0u, 0u, 0u);
+        if (h + r < nh && c0 < dim)
+          nx[r][n] = __ldg(reinterpret_cast<const uint4*>(src + (long long)(h + r) * dim + c0));
+      }
+  };
+  fetch(0);
   float w[NV][VEC], cs[NV][VEC / 2], sn[NV][VEC / 2];
   const bool rot = sd.pos != nullptr;
   const int pos = rot ? sd.pos[row] : 0;
@@ -104,7 +124,14 @@ __global__ void __launch_bounds__(kNormThreads) k_norm_rope(const __grid_constan
   for (int n = 0; n < NV; ++n) {
     const int c0 = (lane + n * G) * VEC;
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) w[n][k] = sd.weight != nullptr && c0 < dim ? sd.weight[c0 + k] : 1.f;
+    for (int k = 0; k < VEC; k += 4) {
+      float4 f = make_float4(1.f, 1.f, 1.f, 1.f);
+      if (sd.weight != nullptr && c0 < dim) f = __ldg(reinterpret_cast<const float4*>(sd.weight + c0 + k));
+      w[n][k] = f.x;
+      w[n][k + 1] = f.y;
+      w[n][k + 2] = f.z;
+      w[n][k + 3] = f.w;
+    }
 #pragma unroll
     for (int k = 0; k < VEC / 2; ++k) {
       const int c = c0 + 2 * k;
@@ -116,40 +143,43 @@ __global__ void __launch_bounds__(kNormThreads) k_norm_rope(const __grid_constan
   const float inv_dim = 1.f / (float)dim;
   // every lane of the warp makes the same number of turns (the shuffles)
   const int turns = sd.hpg;
-  for (int h = 0; h < turns; ++h) {
-    float nx[NV][VEC];
+  for (int h = 0; h < turns; h += kRows) {
+    float v[kRows][NV][VEC], ss[kRows];
 #pragma unroll
-    for (int n = 0; n < NV; ++n) {  // the next head's values
-      const int c0 = (lane + n * G) * VEC;
+    for (int r = 0; r < kRows; ++r) {
+      ss[r] = 0.f;
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) nx[n][k] = 0.f;
-      if (h + 1 < nh && c0 < dim) load16(src + (h + 1) * dim + c0, nx[n]);
-    }
-    float ss = 0.f;
+      for (int n = 0; n < NV; ++n) {
+        norm_values(nx[r][n], v[r][n]);
 #pragma unroll
-    for (int n = 0; n < NV; ++n)
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) ss = fmaf(v[n][k], v[n][k], ss);
-    for (int o = G >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float inv = __frsqrt_rn(fmaf(ss, inv_dim, a.eps));
-#pragma unroll
-    for (int n = 0; n < NV; ++n) {
-      const int c0 = (lane + n * G) * VEC;
-      float y[VEC];
-#pragma unroll
-      for (int k = 0; k < VEC / 2; ++k) {
-        const float p = v[n][2 * k] * inv * w[n][2 * k];
-        const float q = v[n][2 * k + 1] * inv * w[n][2 * k + 1];
-        const bool in = rot && c0 + 2 * k >= rope0;
-        y[2 * k] = in ? p * cs[n][k] - q * sn[n][k] : p;
-        y[2 * k + 1] = in ? p * sn[n][k] + q * cs[n][k] : q;
+        for (int k = 0; k < VEC; ++k) ss[r] = fmaf(v[r][n][k], v[r][n][k], ss[r]);
       }
-      if (store_ok && h < nh && c0 < dim) store16(dst + h * dim + c0, y);
+    }
+    if (h + kRows < turns) fetch(h + kRows);
+    for (int o = G >> 1; o > 0; o >>= 1) {
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) ss[r] += __shfl_xor_sync(0xffffffffu, ss[r], o);
     }
 #pragma unroll
-    for (int n = 0; n < NV; ++n)
+    for (int r = 0; r < kRows; ++r) {
+      const float inv = __frsqrt_rn(fmaf(ss[r], inv_dim, a.eps));
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) v[n][k] = nx[n][k];
+      for (int n = 0; n < NV; ++n) {
+        const int c0 = (lane + n * G) * VEC;
+        float y[VEC];
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) y[k] = v[r][n][k] * inv * w[n][k];
+        if (rot && (n + 1) * G * VEC > rope0) {  // some lane's dims turn (the others' by 1)
+#pragma unroll
+          for (int k = 0; k < VEC; k += 2) {
+            const float p = y[k], q = y[k + 1];
+            y[k] = p * cs[n][k / 2] - q * sn[n][k / 2];
+            y[k + 1] = p * sn[n][k / 2] + q * cs[n][k / 2];
+          }
+        }
+        if (store_ok && h + r < nh && c0 < dim) store16(dst + (long long)(h + r) * dim + c0, y);
+      }
+    }
   }
 }
 
