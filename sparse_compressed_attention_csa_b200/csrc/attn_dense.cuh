@@ -221,8 +221,9 @@ __global__ void __launch_bounds__(kAdThreads, 1)
             const int base = pre + ti - tl;
             sm.u0 = u;
             sm.pre0 = base;
-            sm.g0 = base + (int)((long long)tl * k / cnt);
-            sm.g1 = base + (int)((long long)tl * (k + 1) / cnt);
+            const int each = tl / cnt, more = tl - each * cnt;
+            sm.g0 = base + k * each + min(k, more);
+            sm.g1 = sm.g0 + each + (k < more ? 1 : 0);
             sm.last = pair + cnt - 1 - k;
             found = 1;
           }

@@ -11,10 +11,12 @@
 // a prefill is bound by the epilogue (two instructions per key, token and
 // head on CUDA cores), so NT = 2 gives it eight warps.
 //
-// Roles: warp 0 fetches key tiles into a ring: codes by TMA, one box per page
-// (64-byte swizzle), the 4 scale bytes of each key by cp.async straight into
-// the interleaved order that tcgen05.cp wants (32 rows of 16 B: word c of row
-// l belongs to key l + 32 c), which also takes them through the page table.
+// Roles: warp 0 fetches the codes of key tiles into a ring by TMA, one box per
+// page (64-byte swizzle), and their scales by bulk copies; warp 3 reorders the
+// scales into the rows of 16 B that tcgen05.cp wants (word c of row l belongs
+// to key l + 32 c).  Loading them into that order directly was slower: 4-byte
+// cp.async held the copying warp up for 1,000 clocks a tile, loads through
+// registers (a scoreboard shared with the page lookups) for 3,300.
 // Warp 1 (one thread) copies scales to TMEM and issues the MMAs into a ring
 // of three accumulators.  Warp 2 fetches a unit's queries, their scales and
 // the head weights, two units deep.  Warps 4.. read the accumulators back, in
@@ -52,10 +54,11 @@ struct IdxMxSmem {
   alignas(1024) uint8_t q[2][QU * kImHeads * kImRow];
   alignas(1024) uint8_t keys[STAGES][kImKeys * kImRow];
   alignas(128) uint8_t qs[2][kGroups * 512];
-  alignas(128) uint8_t ks[STAGES][512];
+  alignas(128) uint8_t ks[STAGES][512];   // interleaved, as tcgen05.cp wants them
+  alignas(128) uint8_t raw[STAGES][528];  // in key order, as they are in memory
   alignas(16) float w[2][QU][kImHeads];
   int tiles[kImMaxPlan];
-  uint64_t full[STAGES], empty[STAGES], acc_full[kImBufs], acc_empty[kImBufs];
+  uint64_t full[STAGES], empty[STAGES], raw_full[STAGES], acc_full[kImBufs], acc_empty[kImBufs];
   uint64_t q_full[2], q_empty[2], mma_drain;
   uint32_t tmem_base;
   int abort_flag;
@@ -107,8 +110,9 @@ __global__ void __launch_bounds__(128 + 128 * NT * PAR, MINB)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&sm.full[s], 33);  // lane 0's bytes + 32 lanes' scales
+      mbar_init(&sm.full[s], 2);  // the codes' bytes, the scales
       mbar_init(&sm.empty[s], 1);
+      mbar_init(&sm.raw_full[s], 1);
     }
     for (int i = 0; i < kImBufs; ++i) {
       mbar_init(&sm.acc_full[i], 1);
@@ -128,6 +132,14 @@ __global__ void __launch_bounds__(128 + 128 * NT * PAR, MINB)
   }
   griddep_wait();  // inputs written by the predecessor are visible
   griddep_launch_dependents();
+  // the page table on its way to L2 while the plan is made (a line per CTA)
+  if (a.pm.table != nullptr && warp == 2 && lane == 0) {
+    const long long bytes = (long long)a.B * a.pm.width * 4;
+    for (int i = 0; i < 4; ++i) {
+      const long long at = ((long long)i * gridDim.x + blockIdx.x) * 128;
+      if (at < bytes) asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char*>(a.pm.table) + at));
+    }
+  }
 
   // entries visible to the unit's tokens: lane l's own count (l < nq) and
   // the largest; every lane of the warp takes part
@@ -181,8 +193,9 @@ __global__ void __launch_bounds__(128 + 128 * NT * PAR, MINB)
       const int part = (int)blockIdx.x - (at + inc - cnt);
       if (part >= 0 && part < cnt) {
         pu = u;
-        pb = (int)((long long)tl * part / cnt);
-        pe = (int)((long long)tl * (part + 1) / cnt);
+        const int each = tl / cnt, more = tl - each * cnt;
+        pb = part * each + min(part, more);
+        pe = pb + each + (part < more ? 1 : 0);
       }
       at += __shfl_sync(0xffffffffu, inc, 31);
     }
@@ -248,48 +261,51 @@ __global__ void __launch_bounds__(128 + 128 * NT * PAR, MINB)
     int n = 0;                              // tiles requested
     bool ok = true;
     for (int k = 0; ok && item(k, &it); ++k) {
-      // the rows of a tile's pages, looked up a tile ahead: box `lane` and
-      // keys lane + 32 c
-      struct Rows {
-        long long box, kr[4];
-      };
-      auto rows = [&](int i, Rows* r) {
-        const int j0 = i * kImKeys;
-        const int jb = j0 + lane * a.box_rows;
-        r->box = lane < subs && jb < it.nv ? page_row(a.pm, it.b, a.n_max, jb) : -1;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int j = j0 + lane + 32 * c;
-          r->kr[c] = j < it.nv ? page_row(a.pm, it.b, a.n_max, j) : -1;
-        }
-      };
-      Rows cur, nxt;
-      if (it.tb < it.te) rows(it.tb, &nxt);
+      const bool paged = a.pm.table != nullptr;
+      PageWindow pw;
+      if (paged && it.tb < it.te) pw.start(a.pm, it.b, it.nv, (it.tb * kImKeys) >> a.pm.shift);
       for (int i = it.tb; i < it.te; ++i, ++n) {
         const int s = n % STAGES;
-        cur = nxt;
-        if (i + 1 < it.te) rows(i + 1, &nxt);
+        const int j0 = i * kImKeys;
+        const int jb = j0 + lane * a.box_rows;  // first key of box `lane`
+        long long box = lane < subs && jb < it.nv ? (long long)it.b * a.n_max + jb : -1;
+        if (paged) {
+          pw.seek(j0 >> a.pm.shift);
+          const int pg = pw.at(jb >> a.pm.shift);
+          if (box >= 0)
+            box = (unsigned)pg < (unsigned)a.pm.n_pages
+                      ? ((long long)pg << a.pm.shift) + (jb & ((1 << a.pm.shift) - 1)) : -1;
+        }
         ok = __all_sync(0xffffffffu, mbar_wait_fast(&sm.empty[s], ((uint32_t)(n / STAGES) & 1u) ^ 1u, abortp, wait_ns));
         if (!ok) break;
-        const unsigned boxes = __ballot_sync(0xffffffffu, cur.box >= 0);
-        if (lane == 0)
-          mbar_arrive_expect_tx(&sm.full[s], (uint32_t)__popc(boxes) * (uint32_t)(a.box_rows * kImRow));
+        const unsigned boxes = __ballot_sync(0xffffffffu, box >= 0);
+        // scales: a box's are contiguous; contiguous keys start at a multiple
+        // of four, and end at the last whole 16 bytes of the array
+        long long sc_row = box, sc_bytes = a.box_rows * kImScales;
+        if (!paged) {
+          sc_row = box & ~3LL;
+          sc_bytes = min(528LL, ((long long)a.B * a.n_max - sc_row) * kImScales & ~15LL);
+        }
+        if (lane == 0) {
+          const uint32_t n_box = (uint32_t)__popc(boxes);
+          mbar_arrive_expect_tx(&sm.full[s], n_box * (uint32_t)(a.box_rows * kImRow));
+          mbar_arrive_expect_tx(&sm.raw_full[s], n_box * (uint32_t)sc_bytes);
+        }
         __syncwarp();
-        if (cur.box >= 0)
-          tma_load_2d(sm.keys[s] + lane * a.box_rows * kImRow, &tm_k, &sm.full[s], 0, (int)cur.box);
-        const uint32_t dst = smem_u32(sm.ks[s]) + (uint32_t)lane * 16u;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          cp_async4(dst + 4u * c, cur.kr[c] >= 0 ? a.k_scales + cur.kr[c] * kImScales : a.k_scales, cur.kr[c] >= 0);
-        cp_async_arrive(&sm.full[s]);
+        if (box >= 0) {
+          tma_load_2d(sm.keys[s] + lane * a.box_rows * kImRow, &tm_k, &sm.full[s], 0, (int)box);
+          if (sc_bytes > 0)
+            bulk_load(sm.raw[s] + lane * a.box_rows * kImScales, a.k_scales + sc_row * kImScales,
+                      (uint32_t)sc_bytes, &sm.raw_full[s]);
+        }
       }
     }
     // every copy into shared memory lands before the CTA may exit
-    cp_async_wait_all();
-    __syncwarp();
     if (lane == 0)
-      for (int i = max(0, n - STAGES); i < n; ++i)
+      for (int i = max(0, n - STAGES); i < n; ++i) {
+        mbar_drain(&sm.raw_full[i % STAGES], (uint32_t)(i / STAGES) & 1u, kImDrainNs);
         mbar_drain(&sm.full[i % STAGES], (uint32_t)(i / STAGES) & 1u, kImDrainNs);
+      }
   } else if (warp == 2) {
     // ---------------- queries, their scales and weights
     if (lane == 0) tma_prefetch_desc(&tm_q);
@@ -324,6 +340,41 @@ __global__ void __launch_bounds__(128 + 128 * NT * PAR, MINB)
     if (lane == 0)
       for (int i = max(0, n - 2); i < n; ++i)
         mbar_drain(&sm.q_full[i & 1], (uint32_t)(i >> 1) & 1u, kImDrainNs);
+  } else if (warp == 3) {
+    // ---------------- key scales from key order to rows of 16 bytes: lane l
+    // takes the words of keys l + 32 c
+    int n = 0;
+    bool ok = true;
+    for (int k = 0; ok && item(k, &it); ++k) {
+      for (int i = it.tb; i < it.te; ++i, ++n) {
+        const int s = n % STAGES;
+        ok = __all_sync(0xffffffffu, mbar_wait_fast(&sm.raw_full[s], (uint32_t)(n / STAGES) & 1u, abortp, wait_ns));
+        if (!ok) break;
+        const uint32_t* raw = reinterpret_cast<const uint32_t*>(sm.raw[s]);
+        uint32_t v[4];
+        if (a.pm.table != nullptr) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) v[c] = raw[lane + 32 * c];
+        } else {
+          const long long rows = (long long)a.B * a.n_max;
+          const long long r0 = (long long)it.b * a.n_max + (long long)i * kImKeys, r4 = r0 & ~3LL;
+          const int got = (int)min(132LL, (rows - r4) & ~3LL);  // rows copied
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int at = (int)(r0 - r4) + lane + 32 * c;
+            v[c] = 0u;
+            if (at < got)
+              v[c] = raw[at];
+            else if (r4 + at < rows)  // the array's last one to three
+              v[c] = reinterpret_cast<const uint32_t*>(a.k_scales)[r4 + at];
+          }
+        }
+        *reinterpret_cast<uint4*>(sm.ks[s] + lane * 16) = make_uint4(v[0], v[1], v[2], v[3]);
+        fence_proxy_async_shared();  // read by tcgen05.cp (async proxy)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.full[s]);
+      }
+    }
   } else if (warp == 1) {
     // ---------------- MMA issuer (the whole warp runs the loop, one elected
     // lane issues)
@@ -353,7 +404,6 @@ __global__ void __launch_bounds__(128 + 128 * NT * PAR, MINB)
         const int s = tile % STAGES;
         ok = wait(&sm.full[s], (uint32_t)(tile / STAGES));
         if (!ok) break;
-        fence_proxy_async_shared();
         tc_fence_after();
         // the buffer's last reader, tile - 4, has finished: at least four
         // steps lie between, and the accumulators have three buffers
@@ -401,12 +451,16 @@ __global__ void __launch_bounds__(128 + 128 * NT * PAR, MINB)
       const int qb = n & 1;
       const int blocks = (it.nq + NT - 1) / NT;
       ok = __all_sync(0xffffffffu, mbar_wait_fast(&sm.q_full[qb], (uint32_t)(n >> 1) & 1u, abortp, wait_ns));
+      const bool paged = a.pm.table != nullptr;
+      PageWindow pw;
+      if (paged) pw.start(a.pm, it.b, it.nv, (it.tb * kImKeys) >> a.pm.shift);
       for (int i = it.tb; i < it.te && ok; ++i) {
         const int j = i * kImKeys + quarter * 32 + lane;
         bool in_pool = true;
-        if (a.pm.table != nullptr && j < it.nv) {
-          in_pool = page_row(a.pm, it.b, a.n_max, j) >= 0;
-          if (!in_pool && g == 0) report_error(CSA_ERR_DEVICE_BOUNDS);
+        if (paged) {
+          pw.seek((i * kImKeys) >> a.pm.shift);
+          in_pool = (unsigned)pw.at(j >> a.pm.shift) < (unsigned)a.pm.n_pages;
+          if (!in_pool && j < it.nv && g == 0) report_error(CSA_ERR_DEVICE_BOUNDS);
         }
         for (int nb = 0; nb < blocks; ++nb, ++step) {
           if (PAR > 1 && step % PAR != par) continue;

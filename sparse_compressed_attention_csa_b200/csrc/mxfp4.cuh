@@ -145,6 +145,39 @@ __device__ __forceinline__ long long page_row(const PageMap& pm, int b, int n_ma
   return ((long long)page << pm.shift) + (j & ((1 << pm.shift) - 1));
 }
 
+// A warp's view of one sequence's page table: 32 entries, one per lane, and
+// the next 32 already asked for, so that walking a sequence in order waits for
+// the table once, not at every new line of it.  Entries past the last needed
+// page are not read.
+struct PageWindow {
+  const int32_t* row;  // the sequence's table row
+  int last;            // pages that may be read
+  int w;               // window held in `cur`
+  int cur, nxt;
+  __device__ __forceinline__ int load(int win) const {
+    const int p = win * 32 + (int)(threadIdx.x & 31);
+    return p < last ? row[p] : -1;
+  }
+  // every lane; n: entries of the sequence that will be looked up; page0: first page
+  __device__ __forceinline__ void start(const PageMap& pm, int b, int n, int page0) {
+    row = pm.table + (long long)b * pm.width;
+    last = (int)(((long long)n + (1 << pm.shift) - 1) >> pm.shift);
+    w = page0 >> 5;
+    cur = load(w);
+    nxt = load(w + 1);
+  }
+  // every lane: make the window that holds `page` current (pages only rise)
+  __device__ __forceinline__ void seek(int page) {
+    while (w < (page >> 5)) {
+      cur = nxt;
+      ++w;
+      nxt = load(w + 1);
+    }
+  }
+  // every lane: the table entry of this lane's page, which lies in the window
+  __device__ __forceinline__ int at(int page) const { return __shfl_sync(0xffffffffu, cur, page & 31); }
+};
+
 // Indexer scores on CUDA cores, any head count and dim: one key per thread,
 // the query's dequantized heads and weights in shared memory, 16 heads at a
 // time, 32 dims (one scale) of the key in registers.

@@ -168,9 +168,10 @@ def test_index_scores_of_whole_numbers_are_exact():
     _check_scores(p, t, want, bound, vis, max(len(x[0]) for x in want), exact=True)
 
 
-def test_contiguous_keys_equal_paged_keys():
+@pytest.mark.parametrize("lens", [[3000, 2999, 2997], [2991, 2000, 2992], [9, 8, 10], [530] * 3], ids=str)
+def test_contiguous_keys_equal_paged_keys(lens):
+    # the arrays' row counts leave every remainder by four, and few keys
     p = Params()
-    lens = [3000, 2999, 2997]
     t, want, bound, vis = _score_case(lens, 1, 64, 128, 64, 12)
     n_max = max(len(x[0]) for x in want)
     a = _check_scores(p, t, want, bound, vis, n_max)
