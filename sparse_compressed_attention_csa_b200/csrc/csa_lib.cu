@@ -1398,7 +1398,7 @@ static csa_status_t launch_index_mx(const csa_params_t* p, const uint8_t* q_code
   auto kern = k_index_scores_mx<NT, QU, STAGES, PAR, MINB>;
   const size_t smem = sizeof(IdxMxSmem<NT, QU, STAGES>) + 1024;
   CSA_CHECK(set_smem_attr(kern, smem, "k_index_scores_mx"));
-  const cudaError_t e = launch_ex(kern, dim3((unsigned)grid), dim3(128 + 128 * NT * PAR), smem, s,
+  const cudaError_t e = launch_ex(kern, dim3((unsigned)grid), dim3(160 + 128 * NT * PAR), smem, s,
                                   1, tk, tq, a);
   if (e != cudaSuccess) return cuda_fail(e, "k_index_scores_mx");
   return launched("k_index_scores_mx");
@@ -1415,7 +1415,7 @@ static csa_status_t index_mx_impl(const csa_params_t* p, const uint8_t* q_codes,
   const bool pool = pm.table == nullptr || pm.n_pages > 0;
   if (H_I == kImHeads && d_I == kImDim && pool) {
     if (Tq == 1)
-      return launch_index_mx<1, 1, 8, 1, 2>(p, q_codes, q_scales, w, k_codes, k_scales, pm, q_pos, n_cmp,
+      return launch_index_mx<1, 1, 8, 2, 2>(p, q_codes, q_scales, w, k_codes, k_scales, pm, q_pos, n_cmp,
                                          B, Tq, n_max, scores, s);
     return launch_index_mx<2, 16, 6, 2, 1>(p, q_codes, q_scales, w, k_codes, k_scales, pm, q_pos, n_cmp,
                                         B, Tq, n_max, scores, s);

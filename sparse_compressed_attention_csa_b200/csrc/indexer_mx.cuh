@@ -82,6 +82,26 @@ struct IdxMxArgs {
   float* scores;
 };
 
+// max(0, x) of two values (a NaN stays), packed.
+__device__ __forceinline__ unsigned long long im_relu2(uint32_t lo, uint32_t hi) {
+  unsigned long long r;
+  asm("{\n\t.reg .f32 a, b;\n\t"
+      "max.NaN.f32 a, %1, 0f00000000;\n\t"
+      "max.NaN.f32 b, %2, 0f00000000;\n\t"
+      "mov.b64 %0, {a, b};\n\t}"
+      : "=l"(r)
+      : "f"(__uint_as_float(lo)), "f"(__uint_as_float(hi)));
+  return r;
+}
+
+// Two fp32 fused multiply-adds in one instruction.
+__device__ __forceinline__ unsigned long long im_fma2(unsigned long long a, unsigned long long b,
+                                                      unsigned long long c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
 // Columns: accumulators, key scales, query scales of two units.
 template <int NT, int QU>
 struct IdxMxTmem {
@@ -93,7 +113,7 @@ struct IdxMxTmem {
 };
 
 template <int NT, int QU, int STAGES, int PAR, int MINB>
-__global__ void __launch_bounds__(128 + 128 * NT * PAR, MINB)
+__global__ void __launch_bounds__(160 + 128 * NT * PAR, MINB)
     k_index_scores_mx(const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_q,
                       const __grid_constant__ IdxMxArgs a) {
@@ -254,8 +274,10 @@ __global__ void __launch_bounds__(128 + 128 * NT * PAR, MINB)
   };
 
   Item it;
-  if (warp == 0) {
-    // ---------------- key tiles
+  constexpr int kProducer2 = 4 + 4 * NT * PAR;
+  if (warp == 0 || warp == kProducer2) {
+    // ---------------- key tiles, every second one
+    const int turn = warp == 0 ? 0 : 1;
     if (lane == 0) tma_prefetch_desc(&tm_k);
     const int subs = kImKeys / a.box_rows;  // boxes per tile, at most 16
     int n = 0;                              // tiles requested
@@ -265,6 +287,7 @@ __global__ void __launch_bounds__(128 + 128 * NT * PAR, MINB)
       PageWindow pw;
       if (paged && it.tb < it.te) pw.start(a.pm, it.b, it.nv, (it.tb * kImKeys) >> a.pm.shift);
       for (int i = it.tb; i < it.te; ++i, ++n) {
+        if ((n & 1) != turn) continue;
         const int s = n % STAGES;
         const int j0 = i * kImKeys;
         const int jb = j0 + lane * a.box_rows;  // first key of box `lane`
@@ -301,7 +324,7 @@ __global__ void __launch_bounds__(128 + 128 * NT * PAR, MINB)
       }
     }
     // every copy into shared memory lands before the CTA may exit
-    if (lane == 0)
+    if (lane == 0 && turn == 0)
       for (int i = max(0, n - STAGES); i < n; ++i) {
         mbar_drain(&sm.raw_full[i % STAGES], (uint32_t)(i / STAGES) & 1u, kImDrainNs);
         mbar_drain(&sm.full[i % STAGES], (uint32_t)(i / STAGES) & 1u, kImDrainNs);
@@ -438,7 +461,7 @@ __global__ void __launch_bounds__(128 + 128 * NT * PAR, MINB)
       mbar_drain(&sm.mma_drain, 0, kImDrainNs);
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  } else {
     // ---------------- epilogue: group g takes token g % NT of every PAR-th
     // block (step % PAR = g / NT)
     const int g = (warp - 4) >> 2, quarter = warp & 3;
@@ -471,33 +494,40 @@ __global__ void __launch_bounds__(128 + 128 * NT * PAR, MINB)
           const int tok = nb * NT + tk;
           const int nv = __shfl_sync(0xffffffffu, it.own, tok & 31);  // 0 past nq
           float s[4] = {0.f, 0.f, 0.f, 0.f};
+          auto release = [&]() {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.acc_empty[acc]);
+          };
           if (tok < it.nq) {
+            // 16 heads at a time, the next ones on their way; four sums in two
+            // packed pairs, joined at the end; a NaN passes through the maximum
             const uint32_t col = tmem + lane_base + (uint32_t)(acc * N + tk * kImHeads);
-            // four sums, joined at the end; a NaN passes through the maximum
-            const float4* w = reinterpret_cast<const float4*>(sm.w[qb][tok]);
-            auto relu = [](uint32_t x) {
-              float y;
-              asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(__uint_as_float(x)));
-              return y;
-            };
+            const ulonglong2* w = reinterpret_cast<const ulonglong2*>(sm.w[qb][tok]);
+            uint32_t r[2][16];
+            unsigned long long s01 = 0ull, s23 = 0ull;
+            tmem_ld16(col, r[0]);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              uint32_t r[32];
-              tmem_ld32(col + (uint32_t)(half * 32), r);
-              tmem_wait_ld();
+            for (int c = 0; c < 4; ++c) {
+              tmem_wait_ld16(r[c & 1]);
+              if (c < 3)
+                tmem_ld16(col + (uint32_t)(16 * (c + 1)), r[(c + 1) & 1]);
+              else
+                release();
 #pragma unroll
-              for (int h = 0; h < 8; ++h) {
-                const float4 wh = w[half * 8 + h];
-                s[0] = fmaf(wh.x, relu(r[4 * h]), s[0]);
-                s[1] = fmaf(wh.y, relu(r[4 * h + 1]), s[1]);
-                s[2] = fmaf(wh.z, relu(r[4 * h + 2]), s[2]);
-                s[3] = fmaf(wh.w, relu(r[4 * h + 3]), s[3]);
+              for (int h = 0; h < 4; ++h) {
+                const ulonglong2 wh = w[4 * c + h];
+                s01 = im_fma2(wh.x, im_relu2(r[c & 1][4 * h], r[c & 1][4 * h + 1]), s01);
+                s23 = im_fma2(wh.y, im_relu2(r[c & 1][4 * h + 2], r[c & 1][4 * h + 3]), s23);
               }
             }
+            s[0] = __uint_as_float((uint32_t)s01);
+            s[1] = __uint_as_float((uint32_t)(s01 >> 32));
+            s[2] = __uint_as_float((uint32_t)s23);
+            s[3] = __uint_as_float((uint32_t)(s23 >> 32));
+          } else {
+            release();
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.acc_empty[acc]);
           if (j < nv && in_pool)
             a.scores[((long long)it.b * a.Tq + it.t0 + tok) * a.n_max + j] = (s[0] + s[1]) + (s[2] + s[3]);
         }
