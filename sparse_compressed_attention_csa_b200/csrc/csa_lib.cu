@@ -1361,7 +1361,7 @@ static csa_status_t index_mx_checks(const csa_params_t* p, const uint8_t* q_code
   return check_ptr(n_cmp, "n_cmp");
 }
 
-template <int NT, int QU, int STAGES, int PAR, int MINB>
+template <int QU, int STAGES, int PAR>
 static csa_status_t launch_index_mx(const csa_params_t* p, const uint8_t* q_codes,
                                     const uint8_t* q_scales, const float* w,
                                     const uint8_t* k_codes, const uint8_t* k_scales,
@@ -1382,23 +1382,23 @@ static csa_status_t launch_index_mx(const csa_params_t* p, const uint8_t* q_code
   a.stride = p->stride;
   a.blocks_q = (Tq + QU - 1) / QU;
   a.units = a.blocks_q * B;
-  a.box_rows = pm.table != nullptr && pm.shift < 7 ? 1 << pm.shift : kImKeys;
+  a.box_rows = pm.table != nullptr && pm.shift < 8 ? 1 << pm.shift : kImKeys;
   a.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
   a.scores = scores;
-  const int slots = MINB * num_sms();
-  a.planned = a.units <= std::min(slots, kImMaxPlan);
-  // a planned grid: no more CTAs than there can be key tiles
+  // the plan reads every query position; past one unit of 16 per SM it costs
+  // more than it evens out (8K prefill, 512 units: 158 us planned, 115 in turn)
+  a.planned = a.units <= (QU == 1 ? kImMaxPlan : num_sms());
+  // one CTA per SM, no more than there can be tiles (or units taken whole)
   const long long tiles = (long long)a.units * ((n_max + kImKeys - 1) / kImKeys);
-  const int grid = a.planned ? (int)std::max<long long>(a.units, std::min<long long>(slots, tiles))
-                             : std::min(slots, a.units);
+  const int grid = (int)std::min<long long>(num_sms(), a.planned ? tiles : a.units);
   CUtensorMap tk, tq;
   const uint64_t krows = pm.table != nullptr ? (uint64_t)pm.n_pages << pm.shift : (uint64_t)B * n_max;
   CSA_CHECK(make_tmap_mx(&tk, k_codes, krows, (uint32_t)a.box_rows));
   CSA_CHECK(make_tmap_mx(&tq, q_codes, (uint64_t)B * Tq * kImHeads, kImHeads));
-  auto kern = k_index_scores_mx<NT, QU, STAGES, PAR, MINB>;
-  const size_t smem = sizeof(IdxMxSmem<NT, QU, STAGES>) + 1024;
+  auto kern = k_index_scores_mx<QU, STAGES, PAR>;
+  const size_t smem = sizeof(IdxMxSmem<QU, STAGES>) + 1024;
   CSA_CHECK(set_smem_attr(kern, smem, "k_index_scores_mx"));
-  const cudaError_t e = launch_ex(kern, dim3((unsigned)grid), dim3(160 + 128 * NT * PAR), smem, s,
+  const cudaError_t e = launch_ex(kern, dim3((unsigned)grid), dim3(160 + 128 * PAR), smem, s,
                                   1, tk, tq, a);
   if (e != cudaSuccess) return cuda_fail(e, "k_index_scores_mx");
   return launched("k_index_scores_mx");
@@ -1415,9 +1415,9 @@ static csa_status_t index_mx_impl(const csa_params_t* p, const uint8_t* q_codes,
   const bool pool = pm.table == nullptr || pm.n_pages > 0;
   if (H_I == kImHeads && d_I == kImDim && pool) {
     if (Tq == 1)
-      return launch_index_mx<1, 1, 8, 2, 2>(p, q_codes, q_scales, w, k_codes, k_scales, pm, q_pos, n_cmp,
+      return launch_index_mx<1, 8, 3>(p, q_codes, q_scales, w, k_codes, k_scales, pm, q_pos, n_cmp,
                                          B, Tq, n_max, scores, s);
-    return launch_index_mx<2, 16, 6, 2, 1>(p, q_codes, q_scales, w, k_codes, k_scales, pm, q_pos, n_cmp,
+    return launch_index_mx<16, 4, 3>(p, q_codes, q_scales, w, k_codes, k_scales, pm, q_pos, n_cmp,
                                         B, Tq, n_max, scores, s);
   }
   dim3 grid((unsigned)(((long long)n_max + 127) / 128), (unsigned)Tq, (unsigned)B);

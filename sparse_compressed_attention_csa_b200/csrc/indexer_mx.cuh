@@ -1,34 +1,36 @@
 // Step 2a on 4-bit tensor cores: lightning-indexer scores of MXFP4 queries
 // (64 heads x 128 dims) and paged MXFP4 keys.
 //
-//   D[key][q*64 + h] = sum_c q[q][h][c] k[key][c]   (tcgen05 kind::mxf4: E2M1
-//                      operands, one E8M0 scale per 32 dims, fp32 in TMEM)
-//   s[q][key]        = sum_h w[q][h] max(0, D)       (one key per thread)
+//   D[key][h] = sum_c q[h][c] k[key][c]     (tcgen05 kind::mxf4: E2M1 operands,
+//               one E8M0 scale per 32 dims, fp32 in TMEM)
+//   s[key]    = sum_h w[h] max(0, D[key][h])
 //
-// Keys are the MMA's M (128 per tile), NT tokens x 64 heads its N, the 128
-// dims two K steps of 64.  A key is 64 B of codes and 4 B of scales: decode
-// streams 68 B per key where the bf16 indexer streams 256, and is HBM-bound;
-// a prefill is bound by the epilogue (two instructions per key, token and
-// head on CUDA cores), so NT = 2 gives it eight warps.
+// A tile is 256 keys, two MMAs' M of 128; a step is one tile and one query
+// token, N = 64 heads; the 128 dims are two K steps of 64.  A key is 64 B of
+// codes and 4 B of scales: decode streams 68 B per key where the bf16 indexer
+// streams 256, and is bound by latency and by HBM; a prefill is bound by the
+// epilogue's CUDA-core work, one maximum and half a packed multiply-add per
+// key, token and head.  A thread scores two keys (lane l of both halves of the
+// tile) at a time, so that a head's weight, read from shared memory by every
+// thread, serves twice.
 //
-// Roles: warp 0 fetches the codes of key tiles into a ring by TMA, one box per
-// page (64-byte swizzle), and their scales by bulk copies; warp 3 reorders the
-// scales into the rows of 16 B that tcgen05.cp wants (word c of row l belongs
-// to key l + 32 c).  Loading them into that order directly was slower: 4-byte
-// cp.async held the copying warp up for 1,000 clocks a tile, loads through
-// registers (a scoreboard shared with the page lookups) for 3,300.
-// Warp 1 (one thread) copies scales to TMEM and issues the MMAs into a ring
-// of three accumulators.  Warp 2 fetches a unit's queries, their scales and
-// the head weights, two units deep.  Warps 4.. read the accumulators back, in
-// groups of four warps: one token of the NT, every PAR-th block.
+// Roles: warps 0 and 4 + 4 PAR fetch the codes of every second tile by TMA,
+// one box per page (64-byte swizzle), and their scales by bulk copies; warp 3
+// reorders the scales into the rows of 16 B that tcgen05.cp wants (word c of
+// row l belongs to key l + 32 c).  Loading them into that order directly was
+// slower: 4-byte cp.async held the copying warp up for 1,000 clocks per 128
+// keys, loads through registers (a scoreboard shared with the page lookups)
+// for 3,300.  Warp 1 copies scales to TMEM and issues the MMAs into a ring of
+// three accumulators.  Warp 2 fetches a unit's queries, their scales and the
+// head weights, two units deep.  Warps 4.. read the accumulators back, in PAR
+// groups of four warps that take steps in turn.
 //
-// Work: a unit is up to QU query tokens of one sequence.  With no more units
-// than CTAs, the unit's key tiles are dealt to CTAs by a plan that every CTA
-// makes for itself from the visible counts: the fewest tiles L per CTA for
-// which sum ceil(tiles_u / L) fits the grid, tried at total / (CTAs - units /
-// 2) and taken at total / (CTAs - units), which always fits; so ragged
-// batches load the SMs evenly.  With more units, CTAs are persistent and take
-// units in turn, the last (in a causal prefill, the longest) first.
+// Work: a unit is up to QU query tokens of one sequence.  With at most
+// kImMaxPlan units (decode), the units' tiles form one sequence that is cut
+// into equal ranges, one per CTA, which every CTA finds for itself from the
+// visible counts; so ragged batches load the SMs evenly.  With more units (a
+// prefill), CTAs take whole units in turn, back and forth, the last (the
+// longest under a causal mask) first.
 #pragma once
 #include "common.cuh"
 #include "mxfp4.cuh"
@@ -36,34 +38,32 @@
 
 namespace csa {
 
-constexpr int kImKeys = 128;
+constexpr int kImKeys = 256;           // keys per tile
+constexpr int kImHalf = 128;           // the MMA's M
 constexpr int kImHeads = 64;
 constexpr int kImDim = 128;
 constexpr int kImRow = kImDim / 2;     // bytes of codes per key or query head
 constexpr int kImScales = kImDim / 32;  // scale bytes per key or query head
-constexpr int kImBufs = 3;             // accumulators
-constexpr int kImSfa = 4;              // key-scale buffers in TMEM
-constexpr int kImMaxPlan = 512;        // units a plan may hold
+constexpr int kImBufs = 3;             // accumulators of 128 columns
+constexpr int kImSfa = 4;              // key-scale buffers in TMEM, 8 columns each
+constexpr int kImMaxPlan = 512;        // units whose tiles are dealt evenly
 constexpr uint64_t kImDrainNs = 100000000ull;  // 100 ms for the wind-down waits
 
-template <int NT, int QU, int STAGES>
+template <int QU, int STAGES>
 struct IdxMxSmem {
-  static constexpr int kN = NT * kImHeads;
-  static constexpr int kBlocks = QU / NT;                // MMA N blocks per unit
   static constexpr int kGroups = (QU * kImHeads + 127) / 128;  // 128-row scale groups of a unit
   alignas(1024) uint8_t q[2][QU * kImHeads * kImRow];
   alignas(1024) uint8_t keys[STAGES][kImKeys * kImRow];
   alignas(128) uint8_t qs[2][kGroups * 512];
-  alignas(128) uint8_t ks[STAGES][512];   // interleaved, as tcgen05.cp wants them
-  alignas(128) uint8_t raw[STAGES][528];  // in key order, as they are in memory
+  alignas(128) uint8_t ks[STAGES][2 * 512];  // interleaved, as tcgen05.cp wants them
+  alignas(128) uint8_t raw[STAGES][1040];    // in key order, as they are in memory
   alignas(16) float w[2][QU][kImHeads];
   int tiles[kImMaxPlan];
   uint64_t full[STAGES], empty[STAGES], raw_full[STAGES], acc_full[kImBufs], acc_empty[kImBufs];
   uint64_t q_full[2], q_empty[2], mma_drain;
   uint32_t tmem_base;
   int abort_flag;
-  int plan[3];  // this CTA's unit, first tile and end tile (planned launches)
-  int own[QU];  // entries visible to each of that unit's tokens
+  int u0, pre0, g0, g1;  // planned: first unit, its first tile, the CTA's range of tiles
 };
 
 struct IdxMxArgs {
@@ -76,8 +76,8 @@ struct IdxMxArgs {
   int B, Tq, n_max, width, stride;
   int blocks_q;  // units per sequence
   int units;     // blocks_q * B; unit u is block u / B of sequence u % B
-  int planned;   // one planned item per CTA, else units in turn
-  int box_rows;  // key rows per TMA box (128, or the page size below)
+  int planned;   // ranges of tiles, else units in turn
+  int box_rows;  // key rows per TMA box (256, or the page size below)
   unsigned long long wait_ns;
   float* scores;
 };
@@ -103,24 +103,21 @@ __device__ __forceinline__ unsigned long long im_fma2(unsigned long long a, unsi
 }
 
 // Columns: accumulators, key scales, query scales of two units.
-template <int NT, int QU>
+template <int QU>
 struct IdxMxTmem {
-  static constexpr int kAcc = kImBufs * NT * kImHeads;
+  static constexpr int kAcc = kImBufs * 2 * kImHeads;
   static constexpr int kSfb = ((QU * kImHeads + 127) / 128) * 4;
-  static constexpr int kUsed = kAcc + kImSfa * 4 + 2 * kSfb;
-  static constexpr uint32_t kCols = kUsed <= 256 ? 256 : 512;
-  static_assert(kUsed <= 512, "TMEM columns");
+  static_assert(kAcc + kImSfa * 8 + 2 * kSfb <= 512, "TMEM columns");
 };
 
-template <int NT, int QU, int STAGES, int PAR, int MINB>
-__global__ void __launch_bounds__(160 + 128 * NT * PAR, MINB)
+template <int QU, int STAGES, int PAR>
+__global__ void __launch_bounds__(160 + 128 * PAR, 1)
     k_index_scores_mx(const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_q,
                       const __grid_constant__ IdxMxArgs a) {
   using namespace sm100;
-  using S = IdxMxSmem<NT, QU, STAGES>;
-  using T = IdxMxTmem<NT, QU>;
-  constexpr int N = S::kN;
+  using S = IdxMxSmem<QU, STAGES>;
+  using T = IdxMxTmem<QU>;
   extern __shared__ uint8_t smem_raw[];
   S& sm = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                 ~static_cast<uintptr_t>(1023));
@@ -136,18 +133,18 @@ __global__ void __launch_bounds__(160 + 128 * NT * PAR, MINB)
     }
     for (int i = 0; i < kImBufs; ++i) {
       mbar_init(&sm.acc_full[i], 1);
-      mbar_init(&sm.acc_empty[i], 4 * NT);
+      mbar_init(&sm.acc_empty[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.q_full[i], 33);
-      mbar_init(&sm.q_empty[i], 4 * NT * PAR + 1);
+      mbar_init(&sm.q_empty[i], 4 * PAR + 1);
     }
     mbar_init(&sm.mma_drain, 1);
     sm.abort_flag = 0;
     fence_barrier_init();
   }
   if (warp == 3) {
-    tmem_alloc(&sm.tmem_base, T::kCols);
+    tmem_alloc(&sm.tmem_base, 512);
     tmem_relinquish();
   }
   griddep_wait();  // inputs written by the predecessor are visible
@@ -189,97 +186,78 @@ __global__ void __launch_bounds__(160 + 128 * NT * PAR, MINB)
       total += __reduce_add_sync(0xffffffffu, nv);
     }
     __syncwarp();
-    const int G = (int)gridDim.x;
-    int L = 1;
-    for (int tries = 0; tries < 2; ++tries) {
-      const int room = tries == 0 ? G - a.units / 2 : G - a.units + 1;
-      L = max(1, (total + room - 1) / room);
-      int need = 0;
-      for (int u = lane; u < a.units; u += 32) need += (sm.tiles[u] + L - 1) / L;
-      if (__reduce_add_sync(0xffffffffu, need) <= G) break;
+    const int g0 = (int)((long long)total * blockIdx.x / gridDim.x);
+    const int g1 = (int)((long long)total * (blockIdx.x + 1) / gridDim.x);
+    if (lane == 0) {
+      sm.g0 = g0;
+      sm.g1 = g1;
+      sm.u0 = sm.pre0 = 0;
     }
-    // the unit whose CTAs hold this one, its parts of nearly equal size
-    int at = 0, pu = -1, pb = 0, pe = 0;
-    for (int u0 = 0; u0 < a.units; u0 += 32) {
+    __syncwarp();
+    int at = 0;
+    for (int u0 = 0; g0 < g1 && u0 < a.units; u0 += 32) {  // the unit that holds tile g0
       const int u = u0 + lane;
       const int tl = u < a.units ? sm.tiles[u] : 0;
-      const int cnt = (tl + L - 1) / L;
-      int inc = cnt;
+      int inc = tl;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int up = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += up;
       }
-      const int part = (int)blockIdx.x - (at + inc - cnt);
-      if (part >= 0 && part < cnt) {
-        pu = u;
-        const int each = tl / cnt, more = tl - each * cnt;
-        pb = part * each + min(part, more);
-        pe = pb + each + (part < more ? 1 : 0);
+      if (g0 >= at + inc - tl && g0 < at + inc) {
+        sm.u0 = u;
+        sm.pre0 = at + inc - tl;
       }
       at += __shfl_sync(0xffffffffu, inc, 31);
-    }
-    const unsigned who = __ballot_sync(0xffffffffu, pu >= 0);
-    if (who == 0 ? lane == 0 : pu >= 0) {
-      sm.plan[0] = pu;
-      sm.plan[1] = pb;
-      sm.plan[2] = pe;
-    }
-    __syncwarp();
-    const int u = sm.plan[0];
-    if (u >= 0 && lane < QU) {
-      const int b = u % a.B, t = u / a.B * QU + lane;
-      sm.own[lane] = t < a.Tq ? min(n_visible(a.q_pos[b * a.Tq + t], a.n_cmp[b], a.width, a.stride), a.n_max) : 0;
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
-  const uint32_t t_sfa = tmem + T::kAcc, t_sfb = t_sfa + kImSfa * 4;
+  const uint32_t t_sfa = tmem + T::kAcc, t_sfb = t_sfa + kImSfa * 8;
   volatile int* abortp = &sm.abort_flag;
 
-  // item k of this CTA: a unit and its key tiles [tb, te); false past the end
+  // item k of this CTA: a unit and its tiles [tb, te), possibly none; false
+  // past the end
   struct Item {
     int u, b, t0, nq, own, nv, tb, te;
+    int next, pre;  // planned: the unit to come and its first tile
   };
   auto item = [&](int k, Item* it) -> bool {
     if (a.planned) {
-      if (k > 0 || sm.plan[0] < 0) return false;
-      it->u = sm.plan[0];
+      if (k == 0) {
+        it->next = sm.u0;
+        it->pre = sm.pre0;
+      }
+      if (it->pre >= sm.g1 || sm.g0 >= sm.g1) return false;
+      it->u = it->next++;
+      const int tl = sm.tiles[it->u];
+      it->tb = max(0, sm.g0 - it->pre);
+      it->te = min(tl, sm.g1 - it->pre);
+      it->pre += tl;
     } else {
       // back and forth over the CTAs, so that their sums are near
-      const int c = (k & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x;
-      const long long i = (long long)c + (long long)k * gridDim.x;
       if ((long long)k * gridDim.x >= a.units) return false;
-      it->u = a.units - 1 - (int)i;
-      if (i >= a.units) it->u = -1;
-    }
-    if (it->u < 0) {  // no unit in this turn
-      it->tb = it->te = it->nv = it->nq = it->own = it->b = it->t0 = 0;
-      return true;
+      const int c = (k & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x;
+      it->u = a.units - 1 - (int)((long long)c + (long long)k * gridDim.x);
+      it->tb = it->te = 0;
+      if (it->u < 0) return true;  // no unit in this turn
     }
     it->b = it->u % a.B;
     it->t0 = it->u / a.B * QU;
-    if (a.planned) {
-      it->nq = min(QU, a.Tq - it->t0);
-      it->own = lane < QU ? sm.own[lane] : 0;
-      it->nv = __reduce_max_sync(0xffffffffu, it->own);
-    } else {
-      it->nv = unit_nv(it->u, &it->nq, &it->own);
-    }
-    it->tb = a.planned ? sm.plan[1] : 0;
-    it->te = a.planned ? sm.plan[2] : (it->nv + kImKeys - 1) / kImKeys;
+    it->nv = unit_nv(it->u, &it->nq, &it->own);
+    if (!a.planned) it->te = (it->nv + kImKeys - 1) / kImKeys;
     return true;
   };
 
   Item it;
-  constexpr int kProducer2 = 4 + 4 * NT * PAR;
+  constexpr int kProducer2 = 4 + 4 * PAR;
   if (warp == 0 || warp == kProducer2) {
     // ---------------- key tiles, every second one
     const int turn = warp == 0 ? 0 : 1;
     if (lane == 0) tma_prefetch_desc(&tm_k);
-    const int subs = kImKeys / a.box_rows;  // boxes per tile, at most 16
+    const int subs = kImKeys / a.box_rows;  // boxes per tile, at most 32
     int n = 0;                              // tiles requested
     bool ok = true;
     for (int k = 0; ok && item(k, &it); ++k) {
@@ -307,7 +285,7 @@ __global__ void __launch_bounds__(160 + 128 * NT * PAR, MINB)
         long long sc_row = box, sc_bytes = a.box_rows * kImScales;
         if (!paged) {
           sc_row = box & ~3LL;
-          sc_bytes = min(528LL, ((long long)a.B * a.n_max - sc_row) * kImScales & ~15LL);
+          sc_bytes = min(1040LL, ((long long)a.B * a.n_max - sc_row) * kImScales & ~15LL);
         }
         if (lane == 0) {
           const uint32_t n_box = (uint32_t)__popc(boxes);
@@ -374,25 +352,24 @@ __global__ void __launch_bounds__(160 + 128 * NT * PAR, MINB)
         ok = __all_sync(0xffffffffu, mbar_wait_fast(&sm.raw_full[s], (uint32_t)(n / STAGES) & 1u, abortp, wait_ns));
         if (!ok) break;
         const uint32_t* raw = reinterpret_cast<const uint32_t*>(sm.raw[s]);
-        uint32_t v[4];
-        if (a.pm.table != nullptr) {
+        const long long rows = (long long)a.B * a.n_max;
+        const long long r0 = (long long)it.b * a.n_max + (long long)i * kImKeys, r4 = r0 & ~3LL;
+        const int off = a.pm.table != nullptr ? 0 : (int)(r0 - r4);
+        const int got = a.pm.table != nullptr ? kImKeys : (int)min(260LL, (rows - r4) & ~3LL);  // rows copied
 #pragma unroll
-          for (int c = 0; c < 4; ++c) v[c] = raw[lane + 32 * c];
-        } else {
-          const long long rows = (long long)a.B * a.n_max;
-          const long long r0 = (long long)it.b * a.n_max + (long long)i * kImKeys, r4 = r0 & ~3LL;
-          const int got = (int)min(132LL, (rows - r4) & ~3LL);  // rows copied
+        for (int half = 0; half < 2; ++half) {
+          uint32_t v[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const int at = (int)(r0 - r4) + lane + 32 * c;
+            const int at = off + half * kImHalf + lane + 32 * c;
             v[c] = 0u;
             if (at < got)
               v[c] = raw[at];
-            else if (r4 + at < rows)  // the array's last one to three
+            else if (r4 + at < rows)  // contiguous keys: the array's last one to three
               v[c] = reinterpret_cast<const uint32_t*>(a.k_scales)[r4 + at];
           }
+          *reinterpret_cast<uint4*>(sm.ks[s] + half * 512 + lane * 16) = make_uint4(v[0], v[1], v[2], v[3]);
         }
-        *reinterpret_cast<uint4*>(sm.ks[s] + lane * 16) = make_uint4(v[0], v[1], v[2], v[3]);
         fence_proxy_async_shared();  // read by tcgen05.cp (async proxy)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.full[s]);
@@ -401,18 +378,18 @@ __global__ void __launch_bounds__(160 + 128 * NT * PAR, MINB)
   } else if (warp == 1) {
     // ---------------- MMA issuer (the whole warp runs the loop, one elected
     // lane issues)
-    constexpr uint32_t id0 = idesc_mxf4(128, N, 0), id1 = idesc_mxf4(128, N, 2);
+    constexpr uint32_t id0 = idesc_mxf4(kImHalf, kImHeads, 0), id1 = idesc_mxf4(kImHalf, kImHeads, 2);
     auto wait = [&](uint64_t* bar, uint32_t phase) {
       return __all_sync(0xffffffffu, mbar_wait_fast(bar, phase & 1u, abortp, wait_ns)) != 0;
     };
     const uint32_t q0 = smem_u32(sm.q[0]), k0 = smem_u32(sm.keys[0]);
     const uint32_t qs0 = smem_u32(sm.qs[0]), ks0 = smem_u32(sm.ks[0]);
-    int n = 0, tile = 0, step = 0;
+    int n = 0, tile = 0, acc = 0;
+    uint32_t aph = 0;  // phase of the accumulator ring
     bool ok = true;
     for (int k = 0; ok && item(k, &it); ++k) {
       if (it.te <= it.tb) continue;
       const int qb = n & 1;
-      const int blocks = (it.nq + NT - 1) / NT;
       ok = wait(&sm.q_full[qb], (uint32_t)(n >> 1));
       if (!ok) break;
       fence_proxy_async_shared();  // scales came by cp.async (generic proxy)
@@ -430,28 +407,38 @@ __global__ void __launch_bounds__(160 + 128 * NT * PAR, MINB)
         tc_fence_after();
         // the buffer's last reader, tile - 4, has finished: at least four
         // steps lie between, and the accumulators have three buffers
-        const uint32_t sfa = t_sfa + (uint32_t)((tile % kImSfa) * 4);
-        if (elect_one()) tc_cp_scales(sfa, scale_desc(ks0 + 512u * s));
+        const uint32_t sfa = t_sfa + (uint32_t)((tile % kImSfa) * 8);
+        if (elect_one()) {
+          tc_cp_scales(sfa, scale_desc(ks0 + 1024u * s));
+          tc_cp_scales(sfa + 4, scale_desc(ks0 + 1024u * s + 512u));
+        }
         __syncwarp();
         const uint64_t ka = sw64_desc(k0 + (uint32_t)(s * kImKeys * kImRow), 512);
-        for (int nb = 0; nb < blocks; ++nb, ++step) {
-          const int acc = step % kImBufs;
-          ok = wait(&sm.acc_empty[acc], (uint32_t)(step / kImBufs) ^ 1u);
+        const bool two = i * kImKeys + kImHalf < it.nv;
+        for (int tok = 0; tok < it.nq; ++tok) {
+          ok = wait(&sm.acc_empty[acc], aph ^ 1u);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t d = tmem + (uint32_t)(acc * N);
-          const uint32_t sfb = t_sfb + (uint32_t)(qb * T::kSfb + nb * (N / 32));
-          const uint64_t qa = sw64_desc(q_addr + (uint32_t)(nb * N * kImRow), 512);
+          const uint32_t d = tmem + (uint32_t)(acc * 2 * kImHeads);
+          const uint32_t sfb = t_sfb + (uint32_t)(qb * T::kSfb + tok * 2);
+          const uint64_t qa = sw64_desc(q_addr + (uint32_t)(tok * kImHeads * kImRow), 512);
           if (elect_one()) {
             mma_mxf4(d, ka, qa, id0, sfa, sfb, 0u);
             mma_mxf4(d, ka + 2, qa + 2, id1, sfa, sfb, 1u);  // 32 bytes on
+            if (two) {
+              const uint64_t kb = ka + (uint64_t)(kImHalf * kImRow >> 4);
+              mma_mxf4(d + kImHeads, kb, qa, id0, sfa + 4, sfb, 0u);
+              mma_mxf4(d + kImHeads, kb + 2, qa + 2, id1, sfa + 4, sfb, 1u);
+            }
             tc_commit(&sm.acc_full[acc]);
-            if (nb == blocks - 1) {
+            if (tok == it.nq - 1) {
               tc_commit(&sm.empty[s]);
               if (i == it.te - 1) tc_commit(&sm.q_empty[qb]);
             }
           }
           __syncwarp();
+          acc = acc == kImBufs - 1 ? 0 : acc + 1;
+          aph ^= acc == 0 ? 1u : 0u;
         }
       }
       ++n;
@@ -462,74 +449,89 @@ __global__ void __launch_bounds__(160 + 128 * NT * PAR, MINB)
     }
     __syncwarp();
   } else {
-    // ---------------- epilogue: group g takes token g % NT of every PAR-th
-    // block (step % PAR = g / NT)
-    const int g = (warp - 4) >> 2, quarter = warp & 3;
-    const int tk = g % NT, par = g / NT;
+    // ---------------- epilogue: group `par` of four warps takes every PAR-th step
+    const int par = (warp - 4) >> 2, quarter = warp & 3;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-    int n = 0, step = 0;
+    int n = 0, acc = 0, turn = 0;
+    uint32_t aph = 0;
     bool ok = true;
     for (int k = 0; ok && item(k, &it); ++k) {
       if (it.te <= it.tb) continue;
       const int qb = n & 1;
-      const int blocks = (it.nq + NT - 1) / NT;
       ok = __all_sync(0xffffffffu, mbar_wait_fast(&sm.q_full[qb], (uint32_t)(n >> 1) & 1u, abortp, wait_ns));
       const bool paged = a.pm.table != nullptr;
       PageWindow pw;
       if (paged) pw.start(a.pm, it.b, it.nv, (it.tb * kImKeys) >> a.pm.shift);
+      float* row0 = a.scores + ((long long)it.b * a.Tq + it.t0) * a.n_max;
       for (int i = it.tb; i < it.te && ok; ++i) {
-        const int j = i * kImKeys + quarter * 32 + lane;
-        bool in_pool = true;
+        const int j = i * kImKeys + quarter * 32 + lane;  // and j + 128
+        bool in0 = true, in1 = true;
         if (paged) {
           pw.seek((i * kImKeys) >> a.pm.shift);
-          in_pool = (unsigned)pw.at(j >> a.pm.shift) < (unsigned)a.pm.n_pages;
-          if (!in_pool && j < it.nv && g == 0) report_error(CSA_ERR_DEVICE_BOUNDS);
+          in0 = (unsigned)pw.at(j >> a.pm.shift) < (unsigned)a.pm.n_pages;
+          in1 = (unsigned)pw.at((j + kImHalf) >> a.pm.shift) < (unsigned)a.pm.n_pages;
+          if (par == 0 && ((!in0 && j < it.nv) || (!in1 && j + kImHalf < it.nv)))
+            report_error(CSA_ERR_DEVICE_BOUNDS);
         }
-        for (int nb = 0; nb < blocks; ++nb, ++step) {
-          if (PAR > 1 && step % PAR != par) continue;
-          const int acc = step % kImBufs;
-          ok = __all_sync(0xffffffffu, mbar_wait_fast(&sm.acc_full[acc], (uint32_t)(step / kImBufs) & 1u, abortp, wait_ns));
+        const bool two = i * kImKeys + kImHalf < it.nv;
+        for (int tok = 0; tok < it.nq; ++tok) {
+          const int me = acc;
+          const uint32_t ph = aph;
+          const bool mine = turn == par;
+          acc = acc == kImBufs - 1 ? 0 : acc + 1;
+          aph ^= acc == 0 ? 1u : 0u;
+          turn = turn == PAR - 1 ? 0 : turn + 1;
+          if (!mine) continue;
+          ok = __all_sync(0xffffffffu, mbar_wait_fast(&sm.acc_full[me], ph, abortp, wait_ns));
           if (!ok) break;
           tc_fence_after();
-          const int tok = nb * NT + tk;
-          const int nv = __shfl_sync(0xffffffffu, it.own, tok & 31);  // 0 past nq
-          float s[4] = {0.f, 0.f, 0.f, 0.f};
-          auto release = [&]() {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.acc_empty[acc]);
-          };
-          if (tok < it.nq) {
-            // 16 heads at a time, the next ones on their way; four sums in two
-            // packed pairs, joined at the end; a NaN passes through the maximum
-            const uint32_t col = tmem + lane_base + (uint32_t)(acc * N + tk * kImHeads);
-            const ulonglong2* w = reinterpret_cast<const ulonglong2*>(sm.w[qb][tok]);
-            uint32_t r[2][16];
-            unsigned long long s01 = 0ull, s23 = 0ull;
-            tmem_ld16(col, r[0]);
+          const int nv = __shfl_sync(0xffffffffu, it.own, tok);
+          // 16 heads at a time; two packed pairs of sums per key, joined at the
+          // end; a NaN passes through the maximum
+          const uint32_t col = tmem + lane_base + (uint32_t)(me * 2 * kImHeads);
+          const ulonglong2* w = reinterpret_cast<const ulonglong2*>(sm.w[qb][tok]);
+          unsigned long long x01 = 0ull, x23 = 0ull, y01 = 0ull, y23 = 0ull;
+          if (two) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              tmem_wait_ld16(r[c & 1]);
-              if (c < 3)
-                tmem_ld16(col + (uint32_t)(16 * (c + 1)), r[(c + 1) & 1]);
-              else
-                release();
+              uint32_t r0[16], r1[16];
+              tmem_ld16(col + (uint32_t)(16 * c), r0);
+              tmem_ld16(col + (uint32_t)(kImHeads + 16 * c), r1);
+              tmem_wait_ld16(r0);
+              tmem_wait_ld16(r1);
 #pragma unroll
               for (int h = 0; h < 4; ++h) {
                 const ulonglong2 wh = w[4 * c + h];
-                s01 = im_fma2(wh.x, im_relu2(r[c & 1][4 * h], r[c & 1][4 * h + 1]), s01);
-                s23 = im_fma2(wh.y, im_relu2(r[c & 1][4 * h + 2], r[c & 1][4 * h + 3]), s23);
+                x01 = im_fma2(wh.x, im_relu2(r0[4 * h], r0[4 * h + 1]), x01);
+                x23 = im_fma2(wh.y, im_relu2(r0[4 * h + 2], r0[4 * h + 3]), x23);
+                y01 = im_fma2(wh.x, im_relu2(r1[4 * h], r1[4 * h + 1]), y01);
+                y23 = im_fma2(wh.y, im_relu2(r1[4 * h + 2], r1[4 * h + 3]), y23);
               }
             }
-            s[0] = __uint_as_float((uint32_t)s01);
-            s[1] = __uint_as_float((uint32_t)(s01 >> 32));
-            s[2] = __uint_as_float((uint32_t)s23);
-            s[3] = __uint_as_float((uint32_t)(s23 >> 32));
           } else {
-            release();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t r0[16];
+              tmem_ld16(col + (uint32_t)(16 * c), r0);
+              tmem_wait_ld16(r0);
+#pragma unroll
+              for (int h = 0; h < 4; ++h) {
+                const ulonglong2 wh = w[4 * c + h];
+                x01 = im_fma2(wh.x, im_relu2(r0[4 * h], r0[4 * h + 1]), x01);
+                x23 = im_fma2(wh.y, im_relu2(r0[4 * h + 2], r0[4 * h + 3]), x23);
+              }
+            }
           }
-          if (j < nv && in_pool)
-            a.scores[((long long)it.b * a.Tq + it.t0 + tok) * a.n_max + j] = (s[0] + s[1]) + (s[2] + s[3]);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.acc_empty[me]);
+          auto sum4 = [](unsigned long long p, unsigned long long q) {
+            return (__uint_as_float((uint32_t)p) + __uint_as_float((uint32_t)(p >> 32))) +
+                   (__uint_as_float((uint32_t)q) + __uint_as_float((uint32_t)(q >> 32)));
+          };
+          float* row = row0 + (long long)tok * a.n_max + j;
+          if (j < nv && in0) row[0] = sum4(x01, x23);
+          if (j + kImHalf < nv && in1) row[kImHalf] = sum4(y01, y23);
         }
       }
       __syncwarp();
@@ -541,7 +543,7 @@ __global__ void __launch_bounds__(160 + 128 * NT * PAR, MINB)
   __syncthreads();
   if (warp == 3) {
     tc_fence_after();
-    tmem_dealloc(tmem, T::kCols);
+    tmem_dealloc(tmem, 512);
   }
 }
 
