@@ -32,6 +32,8 @@
 // prefill), CTAs take whole units in turn, back and forth, the last (the
 // longest under a causal mask) first.
 #pragma once
+#include <type_traits>
+
 #include "common.cuh"
 #include "mxfp4.cuh"
 #include "sm100.cuh"
@@ -118,6 +120,9 @@ __global__ void __launch_bounds__(160 + 128 * PAR, 1)
   using namespace sm100;
   using S = IdxMxSmem<QU, STAGES>;
   using T = IdxMxTmem<QU>;
+  // a group waits for its step's accumulator by parity, so the step before it
+  // in that buffer has to have passed: it comes no later than the group's last
+  static_assert(PAR <= kImBufs, "a group would take an older phase for its own");
   extern __shared__ uint8_t smem_raw[];
   S& sm = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                 ~static_cast<uintptr_t>(1023));
@@ -486,45 +491,48 @@ __global__ void __launch_bounds__(160 + 128 * PAR, 1)
           if (!ok) break;
           tc_fence_after();
           const int nv = __shfl_sync(0xffffffffu, it.own, tok);
-          // 16 heads at a time; two packed pairs of sums per key, joined at the
-          // end; a NaN passes through the maximum
+          // 8 heads at a time, the next ones on their way; two packed pairs of
+          // sums per key, joined at the end; a NaN passes through the maximum
           const uint32_t col = tmem + lane_base + (uint32_t)(me * 2 * kImHeads);
           const ulonglong2* w = reinterpret_cast<const ulonglong2*>(sm.w[qb][tok]);
           unsigned long long x01 = 0ull, x23 = 0ull, y01 = 0ull, y23 = 0ull;
-          if (two) {
+          auto score = [&](auto both) {
+            constexpr bool kBoth = decltype(both)::value;
+            uint32_t r[2][2][8];
+            tmem_ld8(col, r[0][0]);
+            if (kBoth) tmem_ld8(col + kImHeads, r[0][1]);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t r0[16], r1[16];
-              tmem_ld16(col + (uint32_t)(16 * c), r0);
-              tmem_ld16(col + (uint32_t)(kImHeads + 16 * c), r1);
-              tmem_wait_ld16(r0);
-              tmem_wait_ld16(r1);
+            for (int c = 0; c < kImHeads / 8; ++c) {
+              uint32_t(&r0)[8] = r[c & 1][0];
+              uint32_t(&r1)[8] = r[c & 1][1];
+              if (kBoth)
+                tmem_wait_ld8(r0, r1);
+              else
+                tmem_wait_ld8(r0);
+              if (c + 1 < kImHeads / 8) {
+                tmem_ld8(col + (uint32_t)(8 * (c + 1)), r[(c + 1) & 1][0]);
+                if (kBoth) tmem_ld8(col + (uint32_t)(kImHeads + 8 * (c + 1)), r[(c + 1) & 1][1]);
+              } else {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.acc_empty[me]);
+              }
 #pragma unroll
-              for (int h = 0; h < 4; ++h) {
-                const ulonglong2 wh = w[4 * c + h];
+              for (int h = 0; h < 2; ++h) {
+                const ulonglong2 wh = w[2 * c + h];
                 x01 = im_fma2(wh.x, im_relu2(r0[4 * h], r0[4 * h + 1]), x01);
                 x23 = im_fma2(wh.y, im_relu2(r0[4 * h + 2], r0[4 * h + 3]), x23);
-                y01 = im_fma2(wh.x, im_relu2(r1[4 * h], r1[4 * h + 1]), y01);
-                y23 = im_fma2(wh.y, im_relu2(r1[4 * h + 2], r1[4 * h + 3]), y23);
+                if (kBoth) {
+                  y01 = im_fma2(wh.x, im_relu2(r1[4 * h], r1[4 * h + 1]), y01);
+                  y23 = im_fma2(wh.y, im_relu2(r1[4 * h + 2], r1[4 * h + 3]), y23);
+                }
               }
             }
-          } else {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t r0[16];
-              tmem_ld16(col + (uint32_t)(16 * c), r0);
-              tmem_wait_ld16(r0);
-#pragma unroll
-              for (int h = 0; h < 4; ++h) {
-                const ulonglong2 wh = w[4 * c + h];
-                x01 = im_fma2(wh.x, im_relu2(r0[4 * h], r0[4 * h + 1]), x01);
-                x23 = im_fma2(wh.y, im_relu2(r0[4 * h + 2], r0[4 * h + 3]), x23);
-              }
-            }
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.acc_empty[me]);
+          };
+          if (two)
+            score(std::true_type{});
+          else
+            score(std::false_type{});
           auto sum4 = [](unsigned long long p, unsigned long long q) {
             return (__uint_as_float((uint32_t)p) + __uint_as_float((uint32_t)(p >> 32))) +
                    (__uint_as_float((uint32_t)q) + __uint_as_float((uint32_t)(q >> 32)));
