@@ -77,6 +77,14 @@ class Params:
             object.__setattr__(self, "_c", cs)
         return cs
 
+    def ref(self):
+        """A pointer to the C struct, kept with it."""
+        r = self.__dict__.get("_ref")
+        if r is None:
+            r = ctypes.byref(self.c())
+            object.__setattr__(self, "_ref", r)
+        return r
+
 
 _lib = None
 _P = ctypes.c_void_p
@@ -447,35 +455,63 @@ def hca_attn_fp8(p: Params, q, q_pos, kv_cmp, cmp_scale, n_cmp, kv_raw, raw_scal
 # The paged, 4-bit serving path.  These calls also check that every tensor is
 # on the current device and that the shapes agree.
 
-def _arg(t, name, dtype, shape, dev):
-    """A contiguous tensor of this dtype and shape (None: any size) on `dev`."""
+def _args(dev, *specs):
+    """Addresses of tensors, each given as (tensor, name, dtype, shape), after
+    checking that every one is contiguous, of that dtype and shape, and on
+    device `dev`."""
+    out = []
+    try:
+        for t, name, dtype, shape in specs:
+            if (t.dtype is not dtype or t.shape != shape or t.get_device() != dev
+                    or not t.is_contiguous()):
+                raise AttributeError
+            out.append(t.data_ptr())
+        return out
+    except AttributeError:
+        pass
+    for t, name, dtype, shape in specs:
+        _refuse(t, name, dtype, shape, dev)
+    raise AssertionError("unreachable")
+
+
+def _refuse(t, name, dtype, shape, dev):
+    """Raises what is wrong with a tensor, if anything."""
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    have = t.shape
-    if len(have) != len(shape) or any(w is not None and w != h for h, w in zip(have, shape)):
-        raise ValueError(f"{name} must have shape {list(shape)}, got {list(have)}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
 
 
-def _device_of(t, name):
-    """The tensor's device, which has to be the current one (the library
-    launches on the current device)."""
+def _shape(t, name, ndim):
+    """The tensor's shape, of `ndim` dims."""
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
+    s = t.shape
+    if len(s) != ndim:
+        raise ValueError(f"{name} must have {ndim} dims, got {list(s)}")
+    return s
+
+
+def _device_of(t, name):
+    """The tensor's device index, which has to be the current device's (the
+    library launches there)."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    dev = t.device
-    if dev.index != torch._C._cuda_getDevice():
-        raise ValueError(f"{name} is on {dev}, the current device is "
-                         f"cuda:{torch._C._cuda_getDevice()}")
+    cur = torch._C._cuda_getDevice()
+    if dev != cur:
+        raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{cur}")
     return dev
 
 
@@ -483,25 +519,36 @@ def _ws_arg(ws, dev):
     """(pointer, bytes) of a workspace tensor or None."""
     if ws is None:
         return None, 0
-    if ws.device != dev:
-        raise ValueError(f"ws is on {ws.device}, expected {dev}")
+    if ws.get_device() != dev:
+        raise ValueError(f"ws is on {ws.device}, expected cuda:{dev}")
     if not ws.is_contiguous():
         raise ValueError("ws must be contiguous")
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
+def _ws_bytes(p, op, B, Tq, n_max, dev):
+    """csa_workspace_size on device `dev`, answers kept with the parameter set."""
+    sizes = p.__dict__.get("_ws")
+    if sizes is None:
+        sizes = {}
+        object.__setattr__(p, "_ws", sizes)
+    nb = sizes.get((op, B, Tq, n_max, dev))
+    if nb is None:
+        if len(sizes) >= 4096:  # a server with ever new sizes
+            sizes.clear()
+        nb = sizes[(op, B, Tq, n_max, dev)] = csa_workspace_size(p, op, B, Tq, n_max)
+    return nb
+
+
 def _head_rows(t, name, dtype, dim, dev):
     """Rows [rows][heads][dim] whose heads are dense, at any row stride."""
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
+    rows, heads, d = _shape(t, name, 3)
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[2] != dim:
-        raise ValueError(f"{name} must have shape [rows, heads, {dim}], got {list(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    rows, heads, _ = t.shape
+    if d != dim:
+        raise ValueError(f"{name} must have heads of {dim}, got {list(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
     sr, sh, sd = t.stride()
     if sd != 1 or (heads > 1 and sh != dim):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
@@ -521,28 +568,43 @@ def csa_norm_rope(p: Params, eps: float, q=None, q_weight=None, q_pos=None, q_ou
     dev = _device_of(first, name)
     dt = first.dtype
     code = _dtype_code(first)
-    if first.dim() != 3:
-        raise ValueError(f"{name} must have 3 dims, got {list(first.shape)}")
-    dim = first.shape[2]
+    dim = _shape(first, name, 3)[2]
     f32, i32 = torch.float32, torch.int32
-    qa = ka = (None, 0, 1, 0, None, None, None)
+    qa = ka = (None, 0, 1, 0)
+    specs = []
     if q is not None:
-        ptr, st, heads, rows = _head_rows(q, "q", dt, dim, dev)
-        qa = (ptr, st, heads, rows,
-              None if q_weight is None else _arg(q_weight, "q_weight", f32, (dim,), dev),
-              None if q_pos is None else _arg(q_pos, "q_pos", i32, (rows,), dev),
-              _arg(q_out, "q_out", dt, (rows, heads, dim), dev))
-    n_out, slots = 0, None
+        qa = _head_rows(q, "q", dt, dim, dev)
+        rows = qa[3]
+        specs.append((q_out, "q_out", dt, (rows, qa[2], dim)))
+        if q_weight is not None:
+            specs.append((q_weight, "q_weight", f32, (dim,)))
+        if q_pos is not None:
+            specs.append((q_pos, "q_pos", i32, (rows,)))
+    n_out = 0
     if k is not None:
-        ptr, st, heads, rows = _head_rows(k, "k", dt, dim, dev)
-        out = _arg(k_out, "k_out", dt, (rows if k_slots is None else None, heads, dim), dev)
-        n_out = k_out.shape[0]
-        slots = None if k_slots is None else _arg(k_slots, "k_slots", i32, (rows,), dev)
-        ka = (ptr, st, heads, rows,
-              None if k_weight is None else _arg(k_weight, "k_weight", f32, (dim,), dev),
-              None if k_pos is None else _arg(k_pos, "k_pos", i32, (rows,), dev), out)
-    _check(_load().csa_norm_rope(ctypes.byref(p.c()), code, dim, eps, *qa, *ka[:6], slots, n_out,
-                                 ka[6], _stream(stream)))
+        ka = _head_rows(k, "k", dt, dim, dev)
+        rows = ka[3]
+        n_out = rows if k_slots is None else _shape(k_out, "k_out", 3)[0]
+        specs.append((k_out, "k_out", dt, (n_out, ka[2], dim)))
+        if k_weight is not None:
+            specs.append((k_weight, "k_weight", f32, (dim,)))
+        if k_pos is not None:
+            specs.append((k_pos, "k_pos", i32, (rows,)))
+        if k_slots is not None:
+            specs.append((k_slots, "k_slots", i32, (rows,)))
+    it = iter(_args(dev, *specs))
+    qo = qw = qp = ko = kw = kp = ks = None
+    if q is not None:
+        qo = next(it)
+        qw = None if q_weight is None else next(it)
+        qp = None if q_pos is None else next(it)
+    if k is not None:
+        ko = next(it)
+        kw = None if k_weight is None else next(it)
+        kp = None if k_pos is None else next(it)
+        ks = None if k_slots is None else next(it)
+    _check(_load().csa_norm_rope(p.ref(), code, dim, eps, *qa, qw, qp, qo, *ka, kw, kp, ks, n_out,
+                                 ko, _stream(stream)))
 
 
 def csa_quantize_mxfp4(rows, codes, scales, slots=None, values=None, stream=None):
@@ -554,60 +616,64 @@ def csa_quantize_mxfp4(rows, codes, scales, slots=None, values=None, stream=None
     import torch
     dev = _device_of(rows, "rows")
     code = _dtype_code(rows)
-    if rows.dim() < 1:
+    have = rows.shape
+    if not have:
         raise ValueError("rows must have at least 1 dim")
-    d = rows.shape[-1]
+    d = have[-1]
     n = rows.numel() // d if d else 0
     if rows.is_contiguous():
         stride = d
-    elif rows.dim() == 2 and rows.stride(1) == 1:
+    elif len(have) == 2 and rows.stride(1) == 1:
         stride = rows.stride(0)
     else:
         raise ValueError("rows must be contiguous, or 2-D with contiguous rows")
-    for t, name, div in ((codes, "codes", 2), (scales, "scales", 32)):
-        _arg(t, name, torch.uint8, (None,) * (t.dim() - 1) + (d // div,), dev)
-    n_out = codes.numel() // (d // 2) if d >= 2 else 0
-    if tuple(codes.shape[:-1]) != tuple(scales.shape[:-1]):
-        raise ValueError("codes and scales must have the same rows")
-    sp = None
+    if not isinstance(codes, torch.Tensor):
+        raise TypeError("codes must be a torch.Tensor")
+    lead = tuple(codes.shape[:-1])
+    specs = [(codes, "codes", torch.uint8, lead + (d // 2,)),
+             (scales, "scales", torch.uint8, lead + (d // 32,))]
     if slots is not None:
-        if rows.dim() != 2:
+        if len(have) != 2:
             raise ValueError("slots need 2-D rows")
-        sp = _arg(slots, "slots", torch.int32, (n,), dev)
-    elif tuple(codes.shape[:-1]) != tuple(rows.shape[:-1]):
+        specs.append((slots, "slots", torch.int32, (n,)))
+    elif lead != tuple(have[:-1]):
         raise ValueError("without slots, codes and scales must have the rows' leading dims")
-    vp = None if values is None else _arg(values, "values", rows.dtype, tuple(rows.shape), dev)
-    _check(_load().csa_quantize_mxfp4(code, rows.data_ptr(), stride, n, d, sp, n_out,
-                                      codes.data_ptr(), scales.data_ptr(), vp, _stream(stream)))
+    if values is not None:
+        specs.append((values, "values", rows.dtype, have))
+    it = _args(dev, *specs)
+    _check(_load().csa_quantize_mxfp4(code, rows.data_ptr(), stride, n, d,
+                                      it[2] if slots is not None else None,
+                                      codes.numel() // (d // 2) if d >= 2 else 0, it[0], it[1],
+                                      it[-1] if values is not None else None, _stream(stream)))
 
 
-def _mx_index_args(p, q_codes, q_scales, w, k_codes, k_scales, page_table, q_pos, n_cmp, n_max):
+def _mx_index_args(p, q_codes, q_scales, w, k_codes, k_scales, page_table, q_pos, n_cmp, n_max,
+                   out, out_name, out_dtype, out_last):
     """Checked arguments of the two indexer calls, in the C order from
-    q_codes to n_max."""
+    q_codes to n_max, then the output."""
     import torch
     dev = _device_of(q_codes, "q_codes")
     u8, i32 = torch.uint8, torch.int32
     H, D = p.idx_heads, p.idx_dim
-    if not isinstance(q_pos, torch.Tensor) or q_pos.dim() != 2:
-        raise ValueError("q_pos must be a [B, Tq] tensor")
-    B, Tq = q_pos.shape
-    qc = _arg(q_codes, "q_codes", u8, (B, Tq, H, D // 2), dev)
-    qs = _arg(q_scales, "q_scales", u8, (B, Tq, H, D // 32), dev)
-    wp = _arg(w, "w", torch.float32, (B, Tq, H), dev)
-    kc = _arg(k_codes, "k_codes", u8, (None, None, D // 2), dev)
-    pages, page = k_codes.shape[0], k_codes.shape[1]
-    ks = _arg(k_scales, "k_scales", u8, (pages, page, D // 32), dev)
+    B, Tq = _shape(q_pos, "q_pos", 2)
+    pages, page, _ = _shape(k_codes, "k_codes", 3)
+    width, tab = 0, ()
     if page_table is None:
         if pages != B or (n_max is not None and page != n_max):
             raise ValueError(f"contiguous keys must be [B, n_max, ...], got {list(k_codes.shape)}")
-        tp, width, n_max = None, 0, page
+        n_max = page
     else:
-        tp = _arg(page_table, "page_table", i32, (B, None), dev)
-        width = page_table.shape[1]
+        width = _shape(page_table, "page_table", 2)[1]
+        tab = ((page_table, "page_table", i32, (B, width)),)
         n_max = width * page if n_max is None else n_max
-    return dev, (qc, qs, wp, kc, ks, tp, width, pages, page,
-                 _arg(q_pos, "q_pos", i32, (B, Tq), dev), _arg(n_cmp, "n_cmp", i32, (B,), dev), B,
-                 Tq, n_max)
+    a = _args(dev, (q_codes, "q_codes", u8, (B, Tq, H, D // 2)),
+              (q_scales, "q_scales", u8, (B, Tq, H, D // 32)), (w, "w", torch.float32, (B, Tq, H)),
+              (k_codes, "k_codes", u8, (pages, page, D // 2)),
+              (k_scales, "k_scales", u8, (pages, page, D // 32)), (q_pos, "q_pos", i32, (B, Tq)),
+              (n_cmp, "n_cmp", i32, (B,)),
+              (out, out_name, out_dtype, (B, Tq, n_max if out_last is None else out_last)), *tab)
+    return dev, (a[0], a[1], a[2], a[3], a[4], a[8] if tab else None, width, pages, page, a[5], a[6],
+                 B, Tq, n_max, a[7])
 
 
 def csa_index_scores_mxfp4(p: Params, q_codes, q_scales, w, k_codes, k_scales, page_table, q_pos,
@@ -616,12 +682,10 @@ def csa_index_scores_mxfp4(p: Params, q_codes, q_scales, w, k_codes, k_scales, p
     [n_pages][page][d_I/2] found through page_table [B][width] (None: keys
     [B][n_max][d_I/2]) -> scores [B][Tq][n_max] of the visible entries."""
     import torch
-    if not isinstance(scores, torch.Tensor) or scores.dim() != 3:
-        raise ValueError("scores must be a [B, Tq, n_max] tensor")
-    dev, a = _mx_index_args(p, q_codes, q_scales, w, k_codes, k_scales, page_table, q_pos, n_cmp,
-                            scores.shape[2])
-    sp = _arg(scores, "scores", torch.float32, (a[11], a[12], a[13]), dev)
-    _check(_load().csa_index_scores_mxfp4(ctypes.byref(p.c()), *a, sp, _stream(stream)))
+    n_max = _shape(scores, "scores", 3)[2]
+    _, a = _mx_index_args(p, q_codes, q_scales, w, k_codes, k_scales, page_table, q_pos, n_cmp,
+                          n_max, scores, "scores", torch.float32, None)
+    _check(_load().csa_index_scores_mxfp4(p.ref(), *a, _stream(stream)))
 
 
 def csa_index_topk_mxfp4(p: Params, q_codes, q_scales, w, k_codes, k_scales, page_table, q_pos,
@@ -631,10 +695,8 @@ def csa_index_topk_mxfp4(p: Params, q_codes, q_scales, w, k_codes, k_scales, pag
     n_max) bytes."""
     import torch
     dev, a = _mx_index_args(p, q_codes, q_scales, w, k_codes, k_scales, page_table, q_pos, n_cmp,
-                            n_max)
-    ip = _arg(idx_out, "idx_out", torch.int32, (a[11], a[12], p.topk), dev)
-    wp, nb = _ws_arg(ws, dev)
-    _check(_load().csa_index_topk_mxfp4(ctypes.byref(p.c()), *a, ip, wp, nb, _stream(stream)))
+                            n_max, idx_out, "idx_out", torch.int32, p.topk)
+    _check(_load().csa_index_topk_mxfp4(p.ref(), *a, *_ws_arg(ws, dev), _stream(stream)))
 
 
 def _attn_paged(fn, p, q, q_pos, kv_pages, page_table, sel, sel_name, sel_shape, kv_raw, raw_pos0,
@@ -643,24 +705,20 @@ def _attn_paged(fn, p, q, q_pos, kv_pages, page_table, sel, sel_name, sel_shape,
     dev = _device_of(q, "q")
     code = _dtype_code(q)
     dt, i32 = q.dtype, torch.int32
-    if not isinstance(q_pos, torch.Tensor) or q_pos.dim() != 2:
-        raise ValueError("q_pos must be a [B, Tq] tensor")
-    B, Tq = q_pos.shape
+    B, Tq = _shape(q_pos, "q_pos", 2)
     H, d = p.n_heads, p.d
-    qp = _arg(q, "q", dt, (B, Tq, H, d), dev)
-    pp = _arg(q_pos, "q_pos", i32, (B, Tq), dev)
-    kp = _arg(kv_pages, "kv_pages", dt, (None, None, d), dev)
-    tp = _arg(page_table, "page_table", i32, (B, None), dev)
-    sp = _arg(sel, sel_name, i32, (B, Tq, p.topk) if sel_shape else (B,), dev)
-    rp = _arg(kv_raw, "kv_raw", dt, (B, None, d), dev)
-    r0 = _arg(raw_pos0, "raw_pos0", i32, (B,), dev)
-    nr = _arg(n_raw, "n_raw", i32, (B,), dev)
-    kp_s = _arg(sink, "sink", torch.float32, (H,), dev)
-    op = _arg(out, "out", dt, (B, Tq, H, d), dev)
-    wp, nb = _ws_arg(ws, dev)
-    _check(fn(ctypes.byref(p.c()), code, qp, pp, kp, kv_pages.shape[0], kv_pages.shape[1], tp,
-              page_table.shape[1], sp, rp, r0, nr, kv_raw.shape[1], kp_s, B, Tq, op, wp, nb,
-              _stream(stream)))
+    pages, page, _ = _shape(kv_pages, "kv_pages", 3)
+    width = _shape(page_table, "page_table", 2)[1]
+    raw_max = _shape(kv_raw, "kv_raw", 3)[1]
+    a = _args(dev, (q, "q", dt, (B, Tq, H, d)), (q_pos, "q_pos", i32, (B, Tq)),
+              (kv_pages, "kv_pages", dt, (pages, page, d)),
+              (page_table, "page_table", i32, (B, width)),
+              (sel, sel_name, i32, (B, Tq, p.topk) if sel_shape else (B,)),
+              (kv_raw, "kv_raw", dt, (B, raw_max, d)), (raw_pos0, "raw_pos0", i32, (B,)),
+              (n_raw, "n_raw", i32, (B,)), (sink, "sink", torch.float32, (H,)),
+              (out, "out", dt, (B, Tq, H, d)))
+    _check(fn(p.ref(), code, a[0], a[1], a[2], pages, page, a[3], width, a[4], a[5], a[6], a[7],
+              raw_max, a[8], B, Tq, a[9], *_ws_arg(ws, dev), _stream(stream)))
 
 
 def csa_sparse_attn_paged(p: Params, q, q_pos, kv_pages, page_table, idx, kv_raw, raw_pos0, n_raw,

@@ -147,6 +147,23 @@ RopeSpec rope_spec(const csa_params_t* p) {
   return r;
 }
 
+// The first n frequencies of a RoPE (0 past its pairs).  pow() takes about 70
+// ns, a call needs 32 of them: each host thread keeps the last set's table.
+void rope_table(const RopeSpec& r, double* out, int n) {
+  constexpr int kMax = 512;
+  static thread_local RopeSpec spec;
+  static thread_local int have = 0;
+  static thread_local double freq[kMax];
+  const bool same = have > 0 && spec.rope_dim == r.rope_dim && spec.theta == r.theta &&
+                    spec.factor == r.factor && spec.orig_ctx == r.orig_ctx &&
+                    spec.beta_fast == r.beta_fast && spec.beta_slow == r.beta_slow;
+  if (!same) have = 0;
+  spec = r;
+  const int pairs = std::min(r.rope_dim / 2, kMax);
+  for (; have < std::min(n, pairs); ++have) freq[have] = rope_freq(r, have);
+  for (int i = 0; i < n; ++i) out[i] = i < pairs ? freq[i] : 0.0;
+}
+
 // Softmax scale of the attention calls: `scale`, times YaRN's temperature
 // (0.1 ln s + 1)^2 under the extended RoPE.
 float attn_scale(const csa_params_t* p) {
@@ -938,7 +955,7 @@ static csa_status_t launch_attn_tc(const csa_params_t* p, const AttnArgs& g, voi
     a.part_o = (__half*)ws;
     a.part_ml = (float*)((char*)ws + o_bytes);
   }
-  for (int i = 0; i < kApMaxRope / 2; ++i) a.freq[i] = i < g.rope_dim / 2 ? rope_freq(g.rope, i) : 0.0;
+  rope_table(g.rope, a.freq, kApMaxRope / 2);
   CUtensorMap tq, to, tc, tr;
   CSA_CHECK(make_tmap_bf16(&tq, g.q, kApDim, (uint64_t)LB * g.Tq * kApHeads, 64, kApHeads));
   CSA_CHECK(make_tmap_bf16(&to, g.out, kApDim, (uint64_t)LB * g.Tq * kApHeads, 32, kApHeads,
@@ -1213,7 +1230,8 @@ CSA_API csa_status_t csa_norm_rope(const csa_params_t* p, csa_dtype_t dtype, int
                 dim, p->rope_dim);
   if (!(eps > 0.f) || !std::isfinite(eps))
     return fail(CSA_ERR_INVALID_ARGUMENT, "eps must be positive and finite");
-  NormRopeArgs a{};
+  NormRopeArgs a;
+  a.side[0] = a.side[1] = NormSide{};
   CSA_CHECK(norm_side(a.side[0], "q", dtype, q, q_stride, q_heads, q_rows, q_weight, q_pos, nullptr,
                       q_rows, q_out, dim));
   CSA_CHECK(norm_side(a.side[1], "k", dtype, k, k_stride, k_heads, k_rows, k_weight, k_pos, k_slots,
@@ -1247,8 +1265,8 @@ CSA_API csa_status_t csa_norm_rope(const csa_params_t* p, csa_dtype_t dtype, int
     if (total > 2147483647LL) return fail(CSA_ERR_UNSUPPORTED_SHAPE, "too many rows");
     sd.blocks = (int)blocks;
   }
-  const RopeSpec rope = rope_spec(p);
-  for (int i = 0; i < a.rope_dim / 2; ++i) a.freq[i] = rope_freq(rope, i);
+  a.rope = rope_spec(p);
+  rope_table(a.rope, a.freq, kNormTable);
   cudaStream_t s = (cudaStream_t)stream;
   // heads at a time: two where a group has several, so that a warp keeps two
   // rows in flight and their shuffles overlap
@@ -1519,7 +1537,7 @@ static csa_status_t paged_attn_simt(const csa_params_t* p, csa_dtype_t dtype, co
     return fail(CSA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes, need %zu", ws_bytes, need);
   if (need > 0) CSA_CHECK(check_ptr(ws, "ws"));
   a.part = (float*)ws;
-  for (int i = 0; i < g.rope_dim / 2; ++i) a.freq[i] = rope_freq(g.rope, i);
+  rope_table(g.rope, a.freq, g.rope_dim / 2);
   const int tokens = g.B * g.Tq;
 #define CSA_PAGED_CASE(D, NKV, HGV)                                                  \
   case D:                                                                            \
@@ -1579,7 +1597,7 @@ static csa_status_t launch_attn_dense(const csa_params_t* p, const AttnArgs& g, 
   a.part_o = (__half*)((char*)ws + w.o);
   a.part_ml = (float*)((char*)ws + w.ml);
   a.desc = (int2*)((char*)ws + w.desc);
-  for (int i = 0; i < kApMaxRope / 2; ++i) a.freq[i] = i < g.rope_dim / 2 ? rope_freq(g.rope, i) : 0.0;
+  rope_table(g.rope, a.freq, kApMaxRope / 2);
   CUtensorMap tq, tkv, tr;
   const uint64_t q_rows = (uint64_t)g.B * g.Tq * g.H;
   CSA_CHECK(make_tmap_bf16(&tq, g.q, kApDim, q_rows, 64, kApHeads));

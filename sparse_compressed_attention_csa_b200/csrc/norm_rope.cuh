@@ -21,7 +21,7 @@
 namespace csa {
 
 constexpr int kNormThreads = 256;
-constexpr int kNormMaxPairs = 512;  // RoPE pairs in the table (rope_dim <= 1024)
+constexpr int kNormTable = 64;  // RoPE pairs whose frequencies come with the launch
 
 // One side (queries or keys) of the call.
 struct NormSide {
@@ -42,7 +42,8 @@ struct NormRopeArgs {
   int dim, rope_dim;
   int group;  // lanes per head row, a power of two
   float eps;
-  double freq[kNormMaxPairs];
+  RopeSpec rope;  // for pairs past the table
+  double freq[kNormTable];
 };
 
 // cos / sin of pos * freq to fp32 accuracy: the angle in half turns is
@@ -137,7 +138,10 @@ __global__ void __launch_bounds__(kNormThreads) k_norm_rope(const __grid_constan
       const int c = c0 + 2 * k;
       cs[n][k] = 1.f;
       sn[n][k] = 0.f;
-      if (rot && c >= rope0 && c < dim) norm_cos_sin(pos, a.freq[(c - rope0) >> 1], &cs[n][k], &sn[n][k]);
+      if (rot && c >= rope0 && c < dim) {
+        const int i = (c - rope0) >> 1;
+        norm_cos_sin(pos, i < kNormTable ? a.freq[i] : rope_freq(a.rope, i), &cs[n][k], &sn[n][k]);
+      }
     }
   }
   const float inv_dim = 1.f / (float)dim;

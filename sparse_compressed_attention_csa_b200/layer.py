@@ -198,8 +198,8 @@ def sparse_attn_paged(p: L.Params, q, q_pos, kv_pages, page_table, idx, kv_raw, 
     if out is None:
         out = torch.empty_like(q)
     B, Tq = q_pos.shape
-    nb = L.csa_workspace_size(p, L.CSA_OP_SPARSE_ATTN_PAGED, B, Tq,
-                              page_table.shape[1] * kv_pages.shape[1])
+    nb = L._ws_bytes(p, L.CSA_OP_SPARSE_ATTN_PAGED, B, Tq, page_table.shape[1] * kv_pages.shape[1],
+                     q.get_device())
     L.csa_sparse_attn_paged(p, q, q_pos, kv_pages, page_table, idx, kv_raw, raw_pos0, n_raw, sink,
                             out, ws.get(nb), stream)
     return out
@@ -213,8 +213,8 @@ def hca_decode_paged(p: L.Params, q, q_pos, kv_pages, page_table, n_cmp, kv_raw,
     if out is None:
         out = torch.empty_like(q)
     B, Tq = q_pos.shape
-    nb = L.csa_workspace_size(p, L.CSA_OP_HCA_ATTN_PAGED, B, Tq,
-                              page_table.shape[1] * kv_pages.shape[1])
+    nb = L._ws_bytes(p, L.CSA_OP_HCA_ATTN_PAGED, B, Tq, page_table.shape[1] * kv_pages.shape[1],
+                     q.get_device())
     L.hca_attn_paged(p, q, q_pos, kv_pages, page_table, n_cmp, kv_raw, raw_pos0, n_raw, sink, out,
                      ws.get(nb), stream)
     return out
@@ -238,7 +238,7 @@ def csa_decode_paged(p: L.Params, q, q_pos, q_idx, w, k_codes, k_scales, n_cmp, 
     q_codes, q_scales = quantize_mxfp4(q_idx, stream)
     if n_max is None:
         n_max = page_table.shape[1] * k_codes.shape[1]
-    nb = L.csa_workspace_size(p, L.CSA_OP_INDEX_TOPK, B, Tq, n_max)
+    nb = L._ws_bytes(p, L.CSA_OP_INDEX_TOPK, B, Tq, n_max, q.get_device())
     L.csa_index_topk_mxfp4(p, q_codes, q_scales, w, k_codes, k_scales, page_table, q_pos, n_cmp,
                            idx, ws.get(nb), n_max, stream)
     return idx, sparse_attn_paged(p, q, q_pos, kv_pages, page_table, idx, kv_raw, raw_pos0, n_raw,
