@@ -1,6 +1,7 @@
-// Step 4 over a paged cache of any length, on tensor cores: shared-KV
-// attention of new tokens (up to 128 heads a group, d = 512, bf16) over every
-// visible entry and the window's raw rows, split over the GPU and joined.
+// Steps 3 and 4 over a paged cache, on tensor cores: shared-KV attention of new
+// tokens (groups of up to 128 heads, d = 512, bf16) over every visible entry of
+// a cache of any length (dense, HCA) or over the selected entries (kSparse,
+// CSA), and the window's raw rows, split over the GPU and joined.
 //
 //   z_i = scale q.r_i,  o = sum_i e^z_i r_i / (e^sink + sum_i e^z_i)
 //
@@ -31,7 +32,10 @@
 // slot: a whole tile by TMA, a box per page, a tile with fewer than 64 rows
 // (or a page outside the pool) row by row with zeros in the missing ones, so
 // that what lies behind the last row is never multiplied; 8 issues the MMAs;
-// 9 fetches Q's other half.
+// 9 fetches Q's other half.  Selected entries are fetched four rows at a time
+// (TMA gather), their numbers read two tiles ahead and their pages one; an
+// unused place in a tile repeats one of its rows and is masked.  The first
+// fetching warp leaves each tile's valid rows as a mask for the softmax.
 //
 // Split: all tiles (64 rows; a token's window tiles, then its entries') form
 // one sequence.  With no more tokens than CTA pairs each pair takes part of
@@ -55,6 +59,7 @@ constexpr int kAdSlotBytes = 32768;    // 64 rows x 256 dims, or 128 heads x 128
 constexpr int kAdChunk = 8192;         // 64 rows x 64 dims
 constexpr int kAdQChunk = 16384;       // 128 heads x 64 dims
 constexpr int kAdThreads = 320;
+constexpr int kAdMasks = 8;            // more tiles than the ring lets the fetch run ahead
 constexpr int kAdSegTiles = 3;         // what changing tokens costs a pair, in tiles
 constexpr int kAdMaxPairs = 128;       // units a one-token-per-pair plan may hold
 constexpr size_t kAdPartHalfs = 2 * (size_t)kApHeads * kApHalf;  // fp16 values of one part
@@ -64,7 +69,9 @@ struct AttnDenseArgs {
   const int* q_pos;
   const __nv_bfloat16* kv;
   PageMap pm;
-  const int* n_cmp;
+  const int* n_cmp;  // dense
+  const int* idx;    // sparse: [tokens][topk]
+  int topk;
   int n_max;
   const __nv_bfloat16* kv_raw;
   const int* raw_pos0;
@@ -92,6 +99,8 @@ struct AdMisc {
   uint64_t full[kAdSlots], empty[kAdSlots];
   uint64_t s_full[2], p_full[2], pv_done[2];
   uint64_t q_full, q_free, q_ready, o_free, mma_drain;
+  uint64_t mask_full[kAdMasks];
+  uint2 mask[kAdMasks];  // valid rows of the tiles in flight
   uint32_t tmem_base;
   int abort_flag;
   int u0, pre0, g0, g1;  // this pair's first unit, that unit's first tile, its range of tiles
@@ -114,12 +123,13 @@ struct AdUnit {
   int win_tiles, tiles;
 };
 
+template <bool kSparse>
 __device__ __forceinline__ AdUnit ad_unit(const AttnDenseArgs& a, int u) {
   AdUnit x;
   x.token = u / a.groups;
   x.b = x.token / a.Tq;
   x.t = a.q_pos[x.token];
-  x.n_sel = max(0, min(n_visible(x.t, a.n_cmp[x.b], a.width, a.stride), a.n_max));
+  x.n_sel = kSparse ? a.topk : max(0, min(n_visible(x.t, a.n_cmp[x.b], a.width, a.stride), a.n_max));
   const int rp0 = a.raw_pos0[x.b];
   const int lo = max(max(0, x.t - a.window + 1), rp0);
   const int hi = min(x.t, rp0 + min(a.n_raw[x.b], a.raw_max) - 1);
@@ -130,6 +140,7 @@ __device__ __forceinline__ AdUnit ad_unit(const AttnDenseArgs& a, int u) {
   return x;
 }
 
+template <bool kSparse>
 __global__ void __launch_bounds__(kAdThreads, 1)
     k_attn_dense(const __grid_constant__ AttnDenseArgs a, const __grid_constant__ CUtensorMap tm_q,
                  const __grid_constant__ CUtensorMap tm_kv,
@@ -162,6 +173,7 @@ __global__ void __launch_bounds__(kAdThreads, 1)
     mbar_init(&sm.q_ready, 128);
     mbar_init(&sm.o_free, 128);
     mbar_init(&sm.mma_drain, 1);
+    for (int i = 0; i < kAdMasks; ++i) mbar_init(&sm.mask_full[i], 1);
     sm.abort_flag = 0;
     fence_barrier_init();
   }
@@ -178,7 +190,7 @@ __global__ void __launch_bounds__(kAdThreads, 1)
     const int ua = min(a.units, (int)threadIdx.x * per), ub = min(a.units, ua + per);
     int mine = 0;
     for (int u = ua; u < ub; ++u) {
-      const int n = ad_unit(a, u).tiles;
+      const int n = ad_unit<kSparse>(a, u).tiles;
       mine += n;
       if (a.units <= a.pairs) sm.tl[u] = n;
     }
@@ -239,7 +251,7 @@ __global__ void __launch_bounds__(kAdThreads, 1)
       if (g0 < g1 && g0 >= inc - mine && g0 < inc) {  // the thread whose units hold tile g0
         int pre = inc - mine, u = ua;
         for (; u < ub; ++u) {
-          const int n = ad_unit(a, u).tiles;
+          const int n = ad_unit<kSparse>(a, u).tiles;
           if (g0 < pre + n) break;
           pre += n;
         }
@@ -269,7 +281,7 @@ __global__ void __launch_bounds__(kAdThreads, 1)
     int seg = 0;
     bool joined = false;
     for (; g < g1 && ok; ++seg) {
-      const AdUnit x = ad_unit(a, u);
+      const AdUnit x = ad_unit<kSparse>(a, u);
       const int tb = g - pre, te = min(x.tiles, g1 - pre);
       const bool first = tb == 0, whole = first && te == x.tiles;
       // ---- RoPE table, then Q: the own dims to TMEM, the other dims in place
@@ -362,24 +374,14 @@ __global__ void __launch_bounds__(kAdThreads, 1)
       // ---- the tiles
       float m_run = -INFINITY, l_run = 0.f;
       const int gt0 = gt;
-      // whether rows lane and lane + 32 of tile i count; looked up a tile
-      // ahead, so that the table's latency is not on the tiles' path
-      auto valid_rows = [&](int i, bool* r0, bool* r1) {
-        const bool win = i < x.win_tiles;
-        const int j = (i - x.win_tiles) * kAdTile + lane;
-        const int cnt = win ? x.n_win - i * kAdTile : x.n_sel - (i - x.win_tiles) * kAdTile;
-        *r0 = lane < cnt && (win || page_row(a.pm, x.b, a.n_max, j) >= 0);
-        *r1 = lane + 32 < cnt && (win || page_row(a.pm, x.b, a.n_max, j + 32) >= 0);
-      };
-      bool nr0, nr1;
-      valid_rows(tb, &nr0, &nr1);
       for (int i = tb; i < te; ++i, ++gt) {
         const int sb = gt & 1;
-        const uint32_t v0 = __ballot_sync(0xffffffffu, nr0), v1 = __ballot_sync(0xffffffffu, nr1);
-        if (i + 1 < te) valid_rows(i + 1, &nr0, &nr1);
         ok = __all_sync(0xffffffffu, mbar_wait_fast(&sm.s_full[sb], (uint32_t)(gt >> 1) & 1u, abortp, wait_ns));
+        ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(&sm.mask_full[gt % kAdMasks],
+                                                          (uint32_t)(gt / kAdMasks) & 1u, abortp, wait_ns));
         if (!ok) break;
         tc_fence_after();
+        const uint2 vm = sm.mask[gt % kAdMasks];
         float z[64];  // q.k, not scaled
         {
           uint32_t ra[32], rb[32];
@@ -392,11 +394,11 @@ __global__ void __launch_bounds__(kAdThreads, 1)
             z[32 + e] = __uint_as_float(rb[e]);
           }
         }
-        if ((v0 & v1) != 0xffffffffu) {
+        if ((vm.x & vm.y) != 0xffffffffu) {
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            if (!((v0 >> e) & 1u)) z[e] = -INFINITY;
-            if (!((v1 >> e) & 1u)) z[32 + e] = -INFINITY;
+            if (!((vm.x >> e) & 1u)) z[e] = -INFINITY;
+            if (!((vm.y >> e) & 1u)) z[32 + e] = -INFINITY;
           }
         }
         float mx[8];
@@ -569,7 +571,7 @@ __global__ void __launch_bounds__(kAdThreads, 1)
       tma_prefetch_desc(&tm_kv);
       tma_prefetch_desc(&tm_raw);
     }
-    int item = 0;
+    int item = 0, gt = 0;
     auto claim = [&](int n) -> bool {
       bool r = true;
       if (lane == 0)
@@ -578,7 +580,7 @@ __global__ void __launch_bounds__(kAdThreads, 1)
     };
     const int subs = kAdTile / a.box_rows;
     while (g < g1 && ok) {
-      const AdUnit x = ad_unit(a, u);
+      const AdUnit x = ad_unit<kSparse>(a, u);
       const int tb = g - pre, te = min(x.tiles, g1 - pre);
       // Q's own dims: two slots of 128 heads x 128 dims
       for (int half = 0; half < 2; ++half, ++item) {
@@ -595,19 +597,91 @@ __global__ void __launch_bounds__(kAdThreads, 1)
           }
         }
       }
-      for (int i = tb; i < te && ok; ++i) {
+      // selected entries: lane l < 16 has rows 4 l + c of a tile; entry numbers
+      // are read two tiles ahead, their table entries one
+      const int* sel = kSparse ? a.idx + (long long)x.token * a.topk : nullptr;
+      auto load_idx = [&](int i, int (&ix)[4]) {
+        const int e = (i - x.win_tiles) * kAdTile + 4 * lane;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          ix[c] = i >= x.win_tiles && i < te && lane < 16 && e + c < a.topk ? sel[e + c] : -1;
+      };
+      auto load_pages = [&](const int (&ix)[4], int (&pg)[4]) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          pg[c] = ix[c] >= 0 && ix[c] < a.n_max
+                      ? a.pm.table[(long long)x.b * a.pm.width + (ix[c] >> a.pm.shift)] : -1;
+      };
+      int ix0[4], ix1[4], ix2[4], pg0[4], pg1[4];
+      if (kSparse) {
+        load_idx(tb, ix0);
+        load_idx(tb + 1, ix1);
+        load_pages(ix0, pg0);
+      }
+      for (int i = tb; i < te && ok; ++i, ++gt) {
         const bool win = i < x.win_tiles;
         const int j0 = (i - x.win_tiles) * kAdTile;
         const int cnt = win ? x.n_win - i * kAdTile : x.n_sel - j0;
-        // boxes of a whole tile, one lane each
-        long long box = -1;
-        bool whole = cnt >= kAdTile;
-        if (whole) {
-          if (win)
-            box = lane == 0 ? (long long)x.raw_row + (long long)i * kAdTile : -1;
-          else if (lane < subs)
-            box = page_row(a.pm, x.b, a.n_max, j0 + lane * a.box_rows);
-          whole = __popc(__ballot_sync(0xffffffffu, box >= 0)) == (win ? 1 : subs);
+        long long box = -1;           // boxes of a whole tile, one lane each
+        int rows[4] = {0, 0, 0, 0};   // gathered rows
+        bool whole = false, gather = false;
+        uint2 vm;
+        if (kSparse && !win) {
+          load_pages(ix1, pg1);
+          load_idx(i + 2, ix2);
+          uint32_t nib = 0;
+          int some = 0;
+#pragma unroll
+          for (int c = 3; c >= 0; --c) {
+            const bool in = (unsigned)pg0[c] < (unsigned)a.pm.n_pages;  // -1 where unused
+            if (!in && ix0[c] >= 0 && q == 0) report_error(CSA_ERR_DEVICE_BOUNDS);
+            if (in) {
+              rows[c] = some = (pg0[c] << a.pm.shift) + (ix0[c] & ((1 << a.pm.shift) - 1));
+              nib |= 1u << c;
+            }
+          }
+          const unsigned any = __ballot_sync(0xffffffffu, nib != 0u);
+          gather = any != 0u;
+          some = __shfl_sync(0xffffffffu, some, gather ? __ffs((int)any) - 1 : 0);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (!((nib >> c) & 1u)) rows[c] = some;
+            ix0[c] = ix1[c];
+            ix1[c] = ix2[c];
+            pg0[c] = pg1[c];
+          }
+          vm.x = __reduce_or_sync(0xffffffffu, lane < 8 ? nib << (4 * lane) : 0u);
+          vm.y = __reduce_or_sync(0xffffffffu, lane >= 8 && lane < 16 ? nib << (4 * (lane - 8)) : 0u);
+        } else {
+          if (kSparse) {  // keep the look-ahead moving through the window's tiles
+            load_pages(ix1, pg1);
+            load_idx(i + 2, ix2);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              ix0[c] = ix1[c];
+              ix1[c] = ix2[c];
+              pg0[c] = pg1[c];
+            }
+          }
+          whole = cnt >= kAdTile;
+          if (whole) {
+            if (win)
+              box = lane == 0 ? (long long)x.raw_row + (long long)i * kAdTile : -1;
+            else if (lane < subs)
+              box = page_row(a.pm, x.b, a.n_max, j0 + lane * a.box_rows);
+            whole = __popc(__ballot_sync(0xffffffffu, box >= 0)) == (win ? 1 : subs);
+          }
+          vm = make_uint2(0xffffffffu, 0xffffffffu);
+          if (!whole) {
+            const bool r0 = lane < cnt && (win || page_row(a.pm, x.b, a.n_max, j0 + lane) >= 0);
+            const bool r1 = lane + 32 < cnt && (win || page_row(a.pm, x.b, a.n_max, j0 + lane + 32) >= 0);
+            vm.x = __ballot_sync(0xffffffffu, r0);
+            vm.y = __ballot_sync(0xffffffffu, r1);
+          }
+        }
+        if (q == 0 && lane == 0) {
+          sm.mask[gt % kAdMasks] = vm;
+          mbar_arrive(&sm.mask_full[gt % kAdMasks]);
         }
 #pragma unroll 1
         for (int half = 0; half < 2; ++half, ++item) {
@@ -616,7 +690,12 @@ __global__ void __launch_bounds__(kAdThreads, 1)
           const int slot = item % kAdSlots;
           const int d0 = (half == 0 ? other0 : dim0) + q * 64;
           uint8_t* dst = ring + slot * kAdSlotBytes + q * kAdChunk;
-          if (whole) {
+          if (kSparse && gather) {
+            if (lane == 0) mbar_arrive_expect_tx(&sm.full[slot], kAdChunk);
+            __syncwarp();
+            if (lane < 16)
+              tma_gather4(dst + lane * 512, &tm_kv, &sm.full[slot], d0, rows[0], rows[1], rows[2], rows[3]);
+          } else if (whole) {
             if (lane == 0) mbar_arrive_expect_tx(&sm.full[slot], kAdChunk);
             __syncwarp();
             if (box >= 0)
@@ -629,21 +708,14 @@ __global__ void __launch_bounds__(kAdThreads, 1)
 #pragma unroll 4
             for (int k = 0; k < 16; ++k) {
               const int r = 4 * k + (lane >> 3);
-              const __nv_bfloat16* src = nullptr;
-              if (r < cnt) {
-                if (win) {
-                  src = a.kv_raw + ((long long)x.raw_row + (long long)i * kAdTile + r) * kApDim;
-                } else {
-                  const long long row = page_row(a.pm, x.b, a.n_max, j0 + r);
-                  if (row >= 0) {
-                    src = a.kv + row * kApDim;
-                  } else if (half == 0 && q == 0 && un == 0) {
-                    report_error(CSA_ERR_DEVICE_BOUNDS);
-                  }
-                }
-              }
-              cp_async16(base + (uint32_t)(r * 128 + ((un ^ (r & 7)) << 4)),
-                         src != nullptr ? src + d0 + un * 8 : a.out, src != nullptr);
+              const bool in = ((r < 32 ? vm.x : vm.y) >> (r & 31)) & 1u;
+              const __nv_bfloat16* src = a.out;  // not read
+              if (in)
+                src = (win ? a.kv_raw + ((long long)x.raw_row + (long long)i * kAdTile + r) * kApDim
+                           : a.kv + page_row(a.pm, x.b, a.n_max, j0 + r) * kApDim) + d0 + un * 8;
+              else if (!kSparse && !win && r < cnt && half == 0 && q == 0 && un == 0)
+                report_error(CSA_ERR_DEVICE_BOUNDS);
+              cp_async16(base + (uint32_t)(r * 128 + ((un ^ (r & 7)) << 4)), src, in);
             }
             cp_async_wait_all();
             fence_proxy_async_shared();  // read by the MMA (async proxy)
@@ -674,7 +746,7 @@ __global__ void __launch_bounds__(kAdThreads, 1)
     };
     int item = 0, gt = 0;
     for (int seg = 0; g < g1 && ok; ++seg) {
-      const AdUnit x = ad_unit(a, u);
+      const AdUnit x = ad_unit<kSparse>(a, u);
       const int n = min(x.tiles, g1 - pre) - (g - pre);
       item += 2;  // Q's own dims
       ok = wait(&sm.q_full, seg) && wait(&sm.q_ready, seg);
@@ -744,7 +816,7 @@ __global__ void __launch_bounds__(kAdThreads, 1)
     if (lane == 0) {
       int seg = 0, sent = 0;
       for (; g < g1 && ok; ++seg) {
-        const AdUnit x = ad_unit(a, u);
+        const AdUnit x = ad_unit<kSparse>(a, u);
         if (seg > 0) ok = mbar_wait_fast(&sm.q_free, (uint32_t)(seg - 1) & 1u, abortp, wait_ns);
         if (!ok) break;
         mbar_arrive_expect_tx(&sm.q_full, 4 * kAdQChunk);

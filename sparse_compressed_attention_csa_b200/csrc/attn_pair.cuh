@@ -56,11 +56,6 @@
 // (code value x row scale, rounded once) in the slot's 128B-swizzled layout
 // and release the slot to the MMA.  The rest of the kernel is the bf16 one.
 //
-// Paged entries (kPaged, CSA): the row list holds pool rows, each selected
-// entry's looked up through the page table while the list is built (the
-// window's tiles are already being gathered); nothing else changes, since
-// rows are gathered one by one anyway.
-//
 // Every mbarrier wait is bounded (a.wait_ns); a wait that runs out records
 // CSA_ERR_DEVICE_TIMEOUT and the CTA winds down: it drains every copy and
 // MMA it issued and every partner store it expects, reaches every cluster
@@ -70,7 +65,6 @@
 #include <cuda_fp8.h>
 
 #include "common.cuh"
-#include "mxfp4.cuh"
 #include "sm100.cuh"
 
 namespace csa {
@@ -121,7 +115,6 @@ struct AttnPairArgs {
   __nv_bfloat16* out;          // splits == 1
   __half* part_o;  // splits > 1: [B*Tq][splits][2][8 slabs][4 units][128][8] O / l, fp16
   float* part_ml;  // [B*Tq][splits][2][2][128]  (m, l) in the log2 domain
-  PageMap pm;      // kPaged: where entry j of a sequence is in kv_cmp
   double freq[kApMaxRope / 2];  // RoPE frequencies theta^(-2i/rope_dim)
 };
 
@@ -238,7 +231,7 @@ __device__ __forceinline__ bool ap_softmax_all(bool ok) {
   return all != 0;
 }
 
-template <bool kHca, bool kFp8, bool kPaged = false>
+template <bool kHca, bool kFp8>
 __global__ void __launch_bounds__(kFp8 ? kApThreadsFp8 : kApThreads, 1)
     k_attn_pair(AttnPairArgs a, const __grid_constant__ CUtensorMap tm_q,
                 const __grid_constant__ CUtensorMap tm_out,
@@ -444,10 +437,6 @@ __global__ void __launch_bounds__(kFp8 ? kApThreadsFp8 : kApThreads, 1)
           report_error(CSA_ERR_DEVICE_BOUNDS);
           jv[e] = -1;
         }
-        if (kPaged && jv[e] >= 0) {  // from here on the pool row
-          jv[e] = (int)page_row(a.pm, b, a.n_max, jv[e]);
-          if (jv[e] < 0) report_error(CSA_ERR_DEVICE_BOUNDS);
-        }
         cnt += jv[e] >= 0 ? 1 : 0;
       }
       int x = cnt;
@@ -469,16 +458,14 @@ __global__ void __launch_bounds__(kFp8 ? kApThreadsFp8 : kApThreads, 1)
 #pragma unroll
       for (int e = 0; e < kMaxE; ++e) {
         if (jv[e] >= 0) {
-          if (off < cap) sm.rows[pw + off] = kPaged ? jv[e] : cmp_y0 + jv[e];
+          if (off < cap) sm.rows[pw + off] = cmp_y0 + jv[e];
           ++off;
         }
       }
       n_sel = min(tot, cap);
     }
     const int ps = (n_sel + 3) & ~3;
-    // masked padding: a row that holds finite values
-    if (kPaged) asm volatile("bar.sync 2, 128;" ::: "memory");  // the first selected row is there
-    for (int k = n_sel + tid; k < ps; k += 128) sm.rows[pw + k] = kPaged ? sm.rows[pw] : cmp_y0;
+    for (int k = n_sel + tid; k < ps; k += 128) sm.rows[pw + k] = cmp_y0;  // masked padding
     if (tid == 0) {
       sm.n_sel = n_sel;
       sm.n_win = n_win;

@@ -492,9 +492,9 @@ bool attn_dense_ok(const csa_params_t* p, csa_dtype_t dtype) {
 
 // CTA pairs of the dense paged kernel: every SM takes one CTA; no more pairs
 // than there can be tiles.
-int attn_dense_pairs(const csa_params_t* p, int B, int Tq, int n_max) {
+int attn_dense_pairs(const csa_params_t* p, bool sparse, int B, int Tq, int n_max) {
   const long long units = (long long)B * Tq * ((p->n_heads + kApHeads - 1) / kApHeads);
-  const long long tiles = ((long long)n_max + kAdTile - 1) / kAdTile +
+  const long long tiles = ((long long)(sparse ? p->topk : n_max) + kAdTile - 1) / kAdTile +
                           ((long long)p->window + kAdTile - 1) / kAdTile;
   return (int)std::max<long long>(1, std::min<long long>(std::min(num_sms() / 2, kAdMaxPairs),
                                                          units * std::max<long long>(1, tiles)));
@@ -503,8 +503,8 @@ int attn_dense_pairs(const csa_params_t* p, int B, int Tq, int n_max) {
 struct DenseWs {
   size_t o, ml, desc, total;
 };
-DenseWs attn_dense_ws(const csa_params_t* p, int B, int Tq, int n_max) {
-  const size_t pairs = (size_t)attn_dense_pairs(p, B, Tq, n_max);
+DenseWs attn_dense_ws(const csa_params_t* p, bool sparse, int B, int Tq, int n_max) {
+  const size_t pairs = (size_t)attn_dense_pairs(p, sparse, B, Tq, n_max);
   DenseWs w;
   w.o = 0;
   w.ml = w.o + 2 * pairs * kAdPartHalfs * sizeof(__half);
@@ -566,12 +566,12 @@ CSA_API csa_status_t csa_workspace_size(const csa_params_t* p, csa_op_t op, int3
     case CSA_OP_SPARSE_ATTN: *bytes = attn_ws_bytes(p, CSA_BF16, false, B, Tq, n_max); return CSA_OK;
     case CSA_OP_HCA_ATTN: *bytes = attn_ws_bytes(p, CSA_BF16, true, B, Tq, n_max); return CSA_OK;
     case CSA_OP_SPARSE_ATTN_PAGED:
-      *bytes = std::max(paged_simt_ws_bytes(p, false, B, Tq, n_max),
-                        attn_ws_bytes(p, CSA_BF16, false, B, Tq, n_max));
+      *bytes = paged_simt_ws_bytes(p, false, B, Tq, n_max);
+      if (attn_dense_ok(p, CSA_BF16)) *bytes = std::max(*bytes, attn_dense_ws(p, true, B, Tq, n_max).total);
       return CSA_OK;
     case CSA_OP_HCA_ATTN_PAGED:
       *bytes = paged_simt_ws_bytes(p, true, B, Tq, n_max);
-      if (attn_dense_ok(p, CSA_BF16)) *bytes = std::max(*bytes, attn_dense_ws(p, B, Tq, n_max).total);
+      if (attn_dense_ok(p, CSA_BF16)) *bytes = std::max(*bytes, attn_dense_ws(p, false, B, Tq, n_max).total);
       return CSA_OK;
   }
   return fail(CSA_ERR_INVALID_ARGUMENT, "bad op %d", (int)op);
@@ -912,9 +912,9 @@ static csa_status_t launch_attn_simt(const AttnArgs& a, csa_dtype_t dtype, cudaS
   return launched("k_attn_simt");
 }
 
-template <bool kHca, bool kFp8 = false, bool kPaged = false>
+template <bool kHca, bool kFp8 = false>
 static csa_status_t launch_attn_tc(const csa_params_t* p, const AttnArgs& g, void* ws,
-                                   size_t ws_bytes, cudaStream_t s, const PageMap& pm = PageMap{}) {
+                                   size_t ws_bytes, cudaStream_t s) {
   const int LB = g.layers * g.B;  // (layer, sequence) rows of the grid
   const int sp = attn_splits(p, kHca, LB, g.Tq, g.n_max);
   const size_t need = attn_ws_bytes(p, CSA_BF16, kHca, LB, g.Tq, g.n_max);
@@ -962,9 +962,7 @@ static csa_status_t launch_attn_tc(const csa_params_t* p, const AttnArgs& g, voi
                            CU_TENSOR_MAP_SWIZZLE_64B));
   // row gathers (one-row boxes of 64 dims); a cache with no rows is never
   // read, and its map is made over q instead
-  a.pm = pm;
-  const uint64_t n_cmp_rows = kPaged ? (uint64_t)pm.n_pages << pm.shift : (uint64_t)g.B * g.n_max;
-  const uint64_t n_raw_rows = (uint64_t)g.B * g.raw_max;
+  const uint64_t n_cmp_rows = (uint64_t)g.B * g.n_max, n_raw_rows = (uint64_t)g.B * g.raw_max;
   const uint64_t n_q_rows = (uint64_t)g.B * g.Tq * kApHeads;
   if (kFp8) {  // E4M3 codes: one-row boxes of 128 dims (128 B)
     CSA_CHECK(make_tmap_u8(&tc, n_cmp_rows ? g.kv_cmp : g.q, kApDim,
@@ -977,9 +975,9 @@ static csa_status_t launch_attn_tc(const csa_params_t* p, const AttnArgs& g, voi
     CSA_CHECK(make_tmap_bf16(&tr, n_raw_rows ? g.kv_raw : g.q, kApDim,
                              n_raw_rows ? n_raw_rows : n_q_rows, 64, 1));
   }
-  CSA_CHECK(set_smem_attr(k_attn_pair<kHca, kFp8, kPaged>, kApSmemBytes, "k_attn_pair"));
+  CSA_CHECK(set_smem_attr(k_attn_pair<kHca, kFp8>, kApSmemBytes, "k_attn_pair"));
   dim3 grid((unsigned)(2 * sp), (unsigned)(LB * g.Tq));
-  cudaError_t e = launch_ex(k_attn_pair<kHca, kFp8, kPaged>, grid,
+  cudaError_t e = launch_ex(k_attn_pair<kHca, kFp8>, grid,
                             dim3(kFp8 ? kApThreadsFp8 : kApThreads), kApSmemBytes, s, 2, a, tq, to,
                             tc, tr);
   if (e != cudaSuccess) return cuda_fail(e, "k_attn_pair");
@@ -1554,9 +1552,10 @@ static csa_status_t paged_attn_simt(const csa_params_t* p, csa_dtype_t dtype, co
   return fail(CSA_ERR_UNSUPPORTED_SHAPE, "d=%d", g.d);
 }
 
+template <bool kSparse>
 static csa_status_t launch_attn_dense(const csa_params_t* p, const AttnArgs& g, const PageMap& pm,
                                       void* ws, size_t ws_bytes, cudaStream_t s) {
-  const DenseWs w = attn_dense_ws(p, g.B, g.Tq, g.n_max);
+  const DenseWs w = attn_dense_ws(p, kSparse, g.B, g.Tq, g.n_max);
   if (ws_bytes < w.total)
     return fail(CSA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes, need %zu", ws_bytes, w.total);
   CSA_CHECK(check_ptr(ws, "ws"));
@@ -1575,7 +1574,7 @@ static csa_status_t launch_attn_dense(const csa_params_t* p, const AttnArgs& g, 
   a.H = g.H;
   a.groups = (g.H + kApHeads - 1) / kApHeads;
   const long long units = (long long)g.B * g.Tq * a.groups;
-  const long long tiles = ((long long)g.n_max + kAdTile - 1) / kAdTile +
+  const long long tiles = ((long long)(kSparse ? g.topk : g.n_max) + kAdTile - 1) / kAdTile +
                           ((long long)g.window + kAdTile - 1) / kAdTile + 1;
   if (units * tiles > 2147483647LL || (long long)g.B * g.raw_max > 2147483647LL ||
       (long long)g.B * g.Tq * g.H > 2147483647LL)
@@ -1586,7 +1585,9 @@ static csa_status_t launch_attn_dense(const csa_params_t* p, const AttnArgs& g, 
   a.width = g.width;
   a.stride = g.stride;
   a.rope_dim = g.rope_dim;
-  a.pairs = attn_dense_pairs(p, g.B, g.Tq, g.n_max);
+  a.pairs = attn_dense_pairs(p, kSparse, g.B, g.Tq, g.n_max);
+  a.idx = g.idx;
+  a.topk = g.topk;
   a.box_rows = pm.shift < 6 ? 1 << pm.shift : kAdTile;
   // a masked logit is -inf times the scale, so the scale is kept above 0: a
   // negative one turns Q's signs, 0 becomes the smallest number (weights of 1)
@@ -1604,10 +1605,10 @@ static csa_status_t launch_attn_dense(const csa_params_t* p, const AttnArgs& g, 
   // a cache with no rows is never read, and its map is made over q instead
   const uint64_t kv_rows = (uint64_t)pm.n_pages << pm.shift, raw_rows = (uint64_t)g.B * g.raw_max;
   CSA_CHECK(make_tmap_bf16(&tkv, kv_rows ? g.kv_cmp : g.q, kApDim, kv_rows ? kv_rows : q_rows, 64,
-                           (uint32_t)a.box_rows));
+                           kSparse ? 1u : (uint32_t)a.box_rows));  // gathers: boxes of one row
   CSA_CHECK(make_tmap_bf16(&tr, raw_rows ? g.kv_raw : g.q, kApDim, raw_rows ? raw_rows : q_rows, 64, kAdTile));
-  CSA_CHECK(set_smem_attr(k_attn_dense, kAdSmemBytes, "k_attn_dense"));
-  cudaError_t e = launch_ex(k_attn_dense, dim3((unsigned)(2 * a.pairs)), dim3(kAdThreads), kAdSmemBytes, s, 1,
+  CSA_CHECK(set_smem_attr(k_attn_dense<kSparse>, kAdSmemBytes, "k_attn_dense"));
+  cudaError_t e = launch_ex(k_attn_dense<kSparse>, dim3((unsigned)(2 * a.pairs)), dim3(kAdThreads), kAdSmemBytes, s, 1,
                             a, tq, tkv, tr);
   if (e != cudaSuccess) return cuda_fail(e, "k_attn_dense");
   CSA_CHECK(launched("k_attn_dense"));
@@ -1650,8 +1651,8 @@ CSA_API csa_status_t csa_sparse_attn_paged(const csa_params_t* p, csa_dtype_t dt
   CSA_CHECK(check_device());
   AttnArgs a = make_attn_args(p, q, q_pos, kv_pages, idx, nullptr, table_width * page_size, kv_raw,
                               raw_pos0, n_raw, raw_max, sink, B, Tq, out);
-  if (attn_tc_ok(p, dtype, false, a.n_max))
-    return launch_attn_tc<false, false, true>(p, a, ws, ws_bytes, (cudaStream_t)stream, pm);
+  if (attn_dense_ok(p, dtype))
+    return launch_attn_dense<true>(p, a, pm, ws, ws_bytes, (cudaStream_t)stream);
   return paged_attn_simt<false>(p, dtype, a, pm, ws, ws_bytes, (cudaStream_t)stream);
 }
 
@@ -1670,7 +1671,8 @@ CSA_API csa_status_t hca_attn_paged(const csa_params_t* p, csa_dtype_t dtype, co
   CSA_CHECK(check_device());
   AttnArgs a = make_attn_args(p, q, q_pos, kv_pages, nullptr, n_cmp, table_width * page_size,
                               kv_raw, raw_pos0, n_raw, raw_max, sink, B, Tq, out);
-  if (attn_dense_ok(p, dtype)) return launch_attn_dense(p, a, pm, ws, ws_bytes, (cudaStream_t)stream);
+  if (attn_dense_ok(p, dtype))
+    return launch_attn_dense<false>(p, a, pm, ws, ws_bytes, (cudaStream_t)stream);
   return paged_attn_simt<true>(p, dtype, a, pm, ws, ws_bytes, (cudaStream_t)stream);
 }
 
