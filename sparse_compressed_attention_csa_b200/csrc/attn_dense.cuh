@@ -32,10 +32,11 @@
 // slot: a whole tile by TMA, a box per page, a tile with fewer than 64 rows
 // (or a page outside the pool) row by row with zeros in the missing ones, so
 // that what lies behind the last row is never multiplied; 8 issues the MMAs;
-// 9 fetches Q's other half.  Selected entries are fetched four rows at a time
-// (TMA gather), their numbers read two tiles ahead and their pages one; an
-// unused place in a tile repeats one of its rows and is masked.  The first
-// fetching warp leaves each tile's valid rows as a mask for the softmax.
+// 9 fetches Q's other half.  Selected entries are fetched by 16-byte cp.async,
+// zeros in unused places, their numbers read two tiles ahead and their pages
+// one (four rows per TMA gather instruction took 3,800 clocks a tile to issue).
+// The first fetching warp leaves each tile's valid rows as a mask for the
+// softmax.
 //
 // Split: all tiles (64 rows; a token's window tiles, then its entries') form
 // one sequence.  With no more tokens than CTA pairs each pair takes part of
@@ -160,7 +161,7 @@ __global__ void __launch_bounds__(kAdThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kAdSlots; ++s) {
-      mbar_init(&sm.full[s], 4);  // the fetching warps
+      mbar_init(&sm.full[s], kSparse ? 128 : 4);  // the fetching lanes / warps
       mbar_init(&sm.empty[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -587,14 +588,12 @@ __global__ void __launch_bounds__(kAdThreads, 1)
         ok = claim(item);
         if (!ok) break;
         const int slot = item % kAdSlots;
-        if (lane == 0) {
-          if (q < 2) {
-            mbar_arrive_expect_tx(&sm.full[slot], kAdQChunk);
-            tma_load_2d(ring + slot * kAdSlotBytes + q * kAdQChunk, &tm_q, &sm.full[slot],
-                        dim0 + half * 128 + q * 64, x.token * a.H + (u % a.groups) * kApHeads);
-          } else {
-            mbar_arrive(&sm.full[slot]);
-          }
+        if (lane == 0 && q < 2) {
+          mbar_arrive_expect_tx(&sm.full[slot], kAdQChunk);
+          tma_load_2d(ring + slot * kAdSlotBytes + q * kAdQChunk, &tm_q, &sm.full[slot],
+                      dim0 + half * 128 + q * 64, x.token * a.H + (u % a.groups) * kApHeads);
+        } else if (kSparse || lane == 0) {
+          mbar_arrive(&sm.full[slot]);
         }
       }
       // selected entries: lane l < 16 has rows 4 l + c of a tile; entry numbers
@@ -623,32 +622,29 @@ __global__ void __launch_bounds__(kAdThreads, 1)
         const int j0 = (i - x.win_tiles) * kAdTile;
         const int cnt = win ? x.n_win - i * kAdTile : x.n_sel - j0;
         long long box = -1;           // boxes of a whole tile, one lane each
-        int rows[4] = {0, 0, 0, 0};   // gathered rows
-        bool whole = false, gather = false;
+        bool whole = false;
         uint2 vm;
+        int rowk[16];                 // kSparse: rows 4 k + lane / 8, -1 where none
         if (kSparse && !win) {
           load_pages(ix1, pg1);
           load_idx(i + 2, ix2);
           uint32_t nib = 0;
-          int some = 0;
-#pragma unroll
-          for (int c = 3; c >= 0; --c) {
-            const bool in = (unsigned)pg0[c] < (unsigned)a.pm.n_pages;  // -1 where unused
-            if (!in && ix0[c] >= 0 && q == 0) report_error(CSA_ERR_DEVICE_BOUNDS);
-            if (in) {
-              rows[c] = some = (pg0[c] << a.pm.shift) + (ix0[c] & ((1 << a.pm.shift) - 1));
-              nib |= 1u << c;
-            }
-          }
-          const unsigned any = __ballot_sync(0xffffffffu, nib != 0u);
-          gather = any != 0u;
-          some = __shfl_sync(0xffffffffu, some, gather ? __ffs((int)any) - 1 : 0);
+          int rows[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            if (!((nib >> c) & 1u)) rows[c] = some;
+            const bool in = (unsigned)pg0[c] < (unsigned)a.pm.n_pages;  // -1 where unused
+            if (!in && ix0[c] >= 0 && q == 0) report_error(CSA_ERR_DEVICE_BOUNDS);
+            rows[c] = in ? (pg0[c] << a.pm.shift) + (ix0[c] & ((1 << a.pm.shift) - 1)) : -1;
+            nib |= in ? 1u << c : 0u;
             ix0[c] = ix1[c];
             ix1[c] = ix2[c];
             pg0[c] = pg1[c];
+          }
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const int r0 = __shfl_sync(0xffffffffu, rows[0], k), r1 = __shfl_sync(0xffffffffu, rows[1], k);
+            const int r2 = __shfl_sync(0xffffffffu, rows[2], k), r3 = __shfl_sync(0xffffffffu, rows[3], k);
+            rowk[k] = lane < 16 ? (lane < 8 ? r0 : r1) : (lane < 24 ? r2 : r3);
           }
           vm.x = __reduce_or_sync(0xffffffffu, lane < 8 ? nib << (4 * lane) : 0u);
           vm.y = __reduce_or_sync(0xffffffffu, lane >= 8 && lane < 16 ? nib << (4 * (lane - 8)) : 0u);
@@ -677,6 +673,11 @@ __global__ void __launch_bounds__(kAdThreads, 1)
             const bool r1 = lane + 32 < cnt && (win || page_row(a.pm, x.b, a.n_max, j0 + lane + 32) >= 0);
             vm.x = __ballot_sync(0xffffffffu, r0);
             vm.y = __ballot_sync(0xffffffffu, r1);
+            if (kSparse) {
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                rowk[k] = 4 * k + (lane >> 3) < cnt ? x.raw_row + i * kAdTile + 4 * k + (lane >> 3) : -1;
+            }
           }
         }
         if (q == 0 && lane == 0) {
@@ -690,21 +691,29 @@ __global__ void __launch_bounds__(kAdThreads, 1)
           const int slot = item % kAdSlots;
           const int d0 = (half == 0 ? other0 : dim0) + q * 64;
           uint8_t* dst = ring + slot * kAdSlotBytes + q * kAdChunk;
-          if (kSparse && gather) {
-            if (lane == 0) mbar_arrive_expect_tx(&sm.full[slot], kAdChunk);
-            __syncwarp();
-            if (lane < 16)
-              tma_gather4(dst + lane * 512, &tm_kv, &sm.full[slot], d0, rows[0], rows[1], rows[2], rows[3]);
+          const int un = lane & 7;
+          const uint32_t base = smem_u32(dst);
+          if (kSparse && !whole) {
+            // lane l copies 16-byte unit l % 8 of rows 4k + l / 8
+            const __nv_bfloat16* src = (win ? a.kv_raw : a.kv) + d0 + un * 8;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const int r = 4 * k + (lane >> 3);
+              cp_async16(base + (uint32_t)(r * 128 + ((un ^ (r & 7)) << 4)),
+                         src + (long long)max(rowk[k], 0) * kApDim, rowk[k] >= 0);
+            }
+            cp_async_arrive(&sm.full[slot]);
           } else if (whole) {
-            if (lane == 0) mbar_arrive_expect_tx(&sm.full[slot], kAdChunk);
+            if (lane == 0)
+              mbar_arrive_expect_tx(&sm.full[slot], kAdChunk);
+            else if (kSparse)
+              mbar_arrive(&sm.full[slot]);
             __syncwarp();
             if (box >= 0)
               tma_load_2d(dst + (win ? 0 : lane * a.box_rows * 128), win ? &tm_raw : &tm_kv,
                           &sm.full[slot], d0, (int)box);
           } else {
-            // row by row: lane l copies 16-byte unit l % 8 of rows 4k + l / 8
-            const int un = lane & 7;
-            const uint32_t base = smem_u32(dst);
+            // row by row
 #pragma unroll 4
             for (int k = 0; k < 16; ++k) {
               const int r = 4 * k + (lane >> 3);
@@ -713,7 +722,7 @@ __global__ void __launch_bounds__(kAdThreads, 1)
               if (in)
                 src = (win ? a.kv_raw + ((long long)x.raw_row + (long long)i * kAdTile + r) * kApDim
                            : a.kv + page_row(a.pm, x.b, a.n_max, j0 + r) * kApDim) + d0 + un * 8;
-              else if (!kSparse && !win && r < cnt && half == 0 && q == 0 && un == 0)
+              else if (!win && r < cnt && half == 0 && q == 0 && un == 0)
                 report_error(CSA_ERR_DEVICE_BOUNDS);
               cp_async16(base + (uint32_t)(r * 128 + ((un ^ (r & 7)) << 4)), src, in);
             }
@@ -730,6 +739,7 @@ __global__ void __launch_bounds__(kAdThreads, 1)
     }
     // every copy into shared memory lands before the CTA may exit (the last
     // one asked of each slot; an earlier one was used before it)
+    cp_async_wait_all();
     __syncwarp();
     if (lane == 0)
       for (int n = max(0, item - kAdSlots); n < item; ++n)
@@ -756,6 +766,7 @@ __global__ void __launch_bounds__(kAdThreads, 1)
           const int i0 = item + 2 * i, s0 = i0 % kAdSlots, s1 = (i0 + 1) % kAdSlots;
           ok = wait(&sm.full[s0], i0 / kAdSlots);
           if (!ok) break;
+          if (kSparse) fence_proxy_async_shared();  // written by cp.async (generic proxy)
           tc_fence_after();
           const uint64_t b0 = sw128_desc(ring_a + s0 * kAdSlotBytes, 16, 1024);
           if (elect_one()) {
@@ -768,6 +779,7 @@ __global__ void __launch_bounds__(kAdThreads, 1)
           __syncwarp();
           ok = wait(&sm.full[s1], (i0 + 1) / kAdSlots);
           if (!ok) break;
+          if (kSparse) fence_proxy_async_shared();
           tc_fence_after();
           const uint64_t b1 = sw128_desc(ring_a + s1 * kAdSlotBytes, 16, 1024);
           if (elect_one()) {

@@ -1605,7 +1605,7 @@ static csa_status_t launch_attn_dense(const csa_params_t* p, const AttnArgs& g, 
   // a cache with no rows is never read, and its map is made over q instead
   const uint64_t kv_rows = (uint64_t)pm.n_pages << pm.shift, raw_rows = (uint64_t)g.B * g.raw_max;
   CSA_CHECK(make_tmap_bf16(&tkv, kv_rows ? g.kv_cmp : g.q, kApDim, kv_rows ? kv_rows : q_rows, 64,
-                           kSparse ? 1u : (uint32_t)a.box_rows));  // gathers: boxes of one row
+                           (uint32_t)a.box_rows));
   CSA_CHECK(make_tmap_bf16(&tr, raw_rows ? g.kv_raw : g.q, kApDim, raw_rows ? raw_rows : q_rows, 64, kAdTile));
   CSA_CHECK(set_smem_attr(k_attn_dense<kSparse>, kAdSmemBytes, "k_attn_dense"));
   cudaError_t e = launch_ex(k_attn_dense<kSparse>, dim3((unsigned)(2 * a.pairs)), dim3(kAdThreads), kAdSmemBytes, s, 1,
