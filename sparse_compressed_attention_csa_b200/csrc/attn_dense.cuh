@@ -67,6 +67,7 @@ constexpr size_t kAdPartHalfs = 2 * (size_t)kApHeads * kApHalf;  // fp16 values 
 constexpr int kAdMl = 3 * kApHeads;    // m, l, scale per CTA of a part
 
 struct AttnDenseArgs {
+  const __nv_bfloat16* q;
   const int* q_pos;
   const __nv_bfloat16* kv;
   PageMap pm;
@@ -184,6 +185,14 @@ __global__ void __launch_bounds__(kAdThreads, 1)
   }
   griddep_wait();  // the predecessor's writes are visible
   griddep_launch_dependents();
+  if (threadIdx.x == 0) {
+    // Q, on its way to L2 while the ranges are found (an equal share per CTA,
+    // in units of 1 KB)
+    const long long rows = (long long)a.units / a.groups * a.H;  // of 512 dims
+    const long long r0 = rows * blockIdx.x / gridDim.x, r1 = rows * (blockIdx.x + 1) / gridDim.x;
+    for (long long r = r0; r < min(r1, r0 + 64); r += 16)
+      prefetch_l2(a.q + r * kApDim, (uint32_t)min(16LL, r1 - r) * kApDim * 2);
+  }
 
   // ---- this pair's range of tiles
   {
@@ -855,89 +864,124 @@ __global__ void __launch_bounds__(kAdThreads, 1)
 // Joins the parts of a unit that more than one pair holds:
 //   M = max(sink, max m_s),  L = 2^(sink - M) + sum l_s 2^(m_s - M)
 //   o = sum (l_s 2^(m_s - M) / L) O_s
-// One CTA of 128 threads per (16 dims, 32 heads, unit).  A warp holds 8 heads
-// x 4 lanes; lane k of a head takes every 4th part, all its loads at once and
-// the maximum as it goes, the four states are joined by shuffles in a fixed
-// order, and lane k finishes 4 of the 16 dims.  No shared memory, so that the
-// CTAs can be resident while the attention kernel ends (it leaves 1 KB).
-constexpr int kAdJoinDims = 16;
-
-__global__ void __launch_bounds__(128) k_attn_dense_join(const __grid_constant__ AttnDenseArgs a) {
-  const int slab = blockIdx.x >> 2;  // 16 dims
-  const int lane = threadIdx.x & 31, k = lane >> 3;
-  const int head = (int)(blockIdx.x & 3) * 32 + (int)(threadIdx.x >> 5) * 8 + (lane & 7);
+// A thread takes 16 dims of a head and every K-th part; K lanes share a head and
+// join their states by shuffles, all in a fixed order.  K is the largest at
+// which the threads are resident at once (a second wave costs as much as the
+// first).  No shared memory, so that CTAs can be resident while the attention
+// kernel ends (it leaves 1 KB).
+template <int K>
+__global__ void __launch_bounds__(128, 8) k_attn_dense_join(const __grid_constant__ AttnDenseArgs a) {
+  constexpr int kHeads = 128 / K;  // per CTA
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int k = lane / (32 / K), step = K;
+  const int slab = (int)blockIdx.x / K;  // 16 dims
+  const int head = (int)blockIdx.x % K * kHeads + warp * (32 / K) + lane % (32 / K);
   const int half = slab >> 4, u8 = (slab & 15) * 2;  // two units of 8 dims
   const int d0 = half * kApHalf + u8 * 8;
   const int rope0 = kApDim - a.rope_dim;
+  const bool by_unit = a.units <= a.pairs;
   sm100::griddep_wait();
   sm100::griddep_launch_dependents();
   const int2 ds = __ldcg(a.desc + blockIdx.y);
-  const bool by_unit = a.units <= a.pairs;
   const int unit = by_unit ? (int)blockIdx.y : ds.x;
   const int pair0 = by_unit ? ds.x : (int)blockIdx.y;
-  // nothing to join (or a launch that gave up before it wrote the list)
-  if (unit < 0 || unit >= a.units || pair0 < 0 || ds.y <= pair0 || ds.y >= a.pairs) return;
-  const int n = ds.y - pair0 + 1;
+  // (a launch that gave up may have written no list)
+  if (unit < 0 || unit >= a.units) return;
   const int token = unit / a.groups, h = (unit % a.groups) * kApHeads + head;
   const bool live = h < a.H;
   const float sink_l2 = live ? a.sink[h] * 1.4426950408889634f : 0.f;
   const int t = a.q_pos[token];
+  if (pair0 < 0 || ds.y <= pair0 || ds.y >= a.pairs) return;  // nothing to join
+  const int n = ds.y - pair0 + 1;
   float m = -INFINITY, L = 0.f, o[16];
 #pragma unroll
   for (int e = 0; e < 16; ++e) o[e] = 0.f;
-#pragma unroll 2
-  for (int s = k; s < n; s += 4) {
-    const size_t pi = (size_t)(2 * (pair0 + s) + (s == 0 ? 1 : 0)) * 2 + half;
-    const float* ml = a.part_ml + pi * kAdMl + head;
-    const uint4* po = reinterpret_cast<const uint4*>(a.part_o + pi * (kAdPartHalfs / 2)) + u8 * kApHeads + head;
-    const float ms = __ldcg(ml), ls = __ldcg(ml + kApHeads), sc = __ldcg(ml + 2 * kApHeads);
-    const uint4 v0 = __ldcg(po), v1 = __ldcg(po + kApHeads);
-    const float mn = fmaxf(m, ms);
-    const float old = m == -INFINITY ? 0.f : exp2f(m - mn);
-    const float w = ms == -INFINITY ? 0.f : ls * exp2f(ms - mn);
-    m = mn;
-    L = fmaf(L, old, w);
-    const float ws = w * sc;
-    const uint32_t hv[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+  for (int s0 = k; s0 < n; s0 += 2 * step) {
+    float ms[2], ls[2], sc[2];
+    uint4 v[2][2];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float2 f = ap_f16x2_to_f32(hv[e]);
-      o[2 * e] = fmaf(f.x, ws, o[2 * e] * old);
-      o[2 * e + 1] = fmaf(f.y, ws, o[2 * e + 1] * old);
+    for (int i = 0; i < 2; ++i) {
+      const int s = s0 + i * step;
+      ms[i] = -INFINITY;
+      ls[i] = sc[i] = 0.f;
+      v[i][0] = v[i][1] = make_uint4(0u, 0u, 0u, 0u);
+      if (s < n) {
+        const size_t pi = (size_t)(2 * (pair0 + s) + (s == 0 ? 1 : 0)) * 2 + half;
+        const float* ml = a.part_ml + pi * kAdMl + head;
+        const uint4* po = reinterpret_cast<const uint4*>(a.part_o + pi * (kAdPartHalfs / 2)) + u8 * kApHeads + head;
+        ms[i] = __ldcg(ml);
+        ls[i] = __ldcg(ml + kApHeads);
+        sc[i] = __ldcg(ml + 2 * kApHeads);
+        v[i][0] = __ldcg(po);
+        v[i][1] = __ldcg(po + kApHeads);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float mn = fmaxf(m, ms[i]);
+      const float old = m == -INFINITY ? 0.f : exp2f(m - mn);
+      const float w = ms[i] == -INFINITY ? 0.f : ls[i] * exp2f(ms[i] - mn);
+      m = mn;
+      L = fmaf(L, old, w);
+      const float ws = w * sc[i];
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const uint32_t hv[4] = {v[i][g].x, v[i][g].y, v[i][g].z, v[i][g].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = ap_f16x2_to_f32(hv[e]);
+          o[8 * g + 2 * e] = fmaf(f.x, ws, o[8 * g + 2 * e] * old);
+          o[8 * g + 2 * e + 1] = fmaf(f.y, ws, o[8 * g + 2 * e + 1] * old);
+        }
+      }
     }
   }
-  // the four lanes of the head
-  float M = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-  M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
+  // the head's lanes, and the sink
+  float M = m;
+#pragma unroll
+  for (int x = 32 / K; x < 32; x <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
   M = fmaxf(M, sink_l2);
   const float f = m == -INFINITY ? 0.f : exp2f(m - M);
   L *= f;
-  L += __shfl_xor_sync(0xffffffffu, L, 8);
-  L += __shfl_xor_sync(0xffffffffu, L, 16);
+#pragma unroll
+  for (int x = 32 / K; x < 32; x <<= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
   L += sink_l2 == -INFINITY ? 0.f : exp2f(sink_l2 - M);
   const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
-  float y[4];
+  // lane k finishes 16 / K of the dims: the inverse rotation at -t, bf16
+  constexpr int kMine = 16 / K;
+  float y[kMine];
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
     float v = o[e] * f;
-    v += __shfl_xor_sync(0xffffffffu, v, 8);
-    v += __shfl_xor_sync(0xffffffffu, v, 16);
-    if ((e >> 2) == k) y[e & 3] = v * inv;
-  }
-  const int d = d0 + 4 * k;
 #pragma unroll
-  for (int e = 0; e < 4; e += 2) {
-    if (d + e >= rope0) {  // inverse rotation at -t
+    for (int x = 32 / K; x < 32; x <<= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
+    if (e / kMine == k) y[e % kMine] = v * inv;
+  }
+  const int dm = d0 + kMine * k;
+#pragma unroll
+  for (int e = 0; e < kMine; e += 2) {
+    if (dm + e >= rope0) {
       float c, s;
-      rope_cs_reduced(t, a.freq[(d + e - rope0) >> 1], &c, &s);
+      rope_cs_reduced(t, a.freq[(dm + e - rope0) >> 1], &c, &s);
       const float x0 = y[e], x1 = y[e + 1];
       y[e] = x0 * c + x1 * s;
       y[e + 1] = -x0 * s + x1 * c;
     }
   }
-  if (live)
-    *reinterpret_cast<uint2*>(a.out + ((size_t)token * a.H + h) * kApDim + d) =
-        make_uint2(ap_bf16x2(y[0], y[1]), ap_bf16x2(y[2], y[3]));
+  if (!live) return;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + ((size_t)token * a.H + h) * kApDim + dm);
+  uint32_t w[kMine / 2];
+#pragma unroll
+  for (int e = 0; e < kMine / 2; ++e) w[e] = ap_bf16x2(y[2 * e], y[2 * e + 1]);
+  if (K == 8)
+    dst[0] = w[0];
+  else if (K == 4)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[kMine / 2 - 1]);
+  else
+#pragma unroll
+    for (int e = 0; e < kMine / 2; e += 4)
+      *reinterpret_cast<uint4*>(dst + e) = make_uint4(w[e], w[(e + 1) % (kMine / 2)], w[(e + 2) % (kMine / 2)],
+                                                      w[(e + 3) % (kMine / 2)]);
 }
 
 }  // namespace csa

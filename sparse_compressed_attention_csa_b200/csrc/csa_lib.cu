@@ -12,6 +12,7 @@
 #include <cstdio>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include "attn_dense.cuh"
 #include "attn_paged_simt.cuh"
@@ -1560,6 +1561,7 @@ static csa_status_t launch_attn_dense(const csa_params_t* p, const AttnArgs& g, 
     return fail(CSA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes, need %zu", ws_bytes, w.total);
   CSA_CHECK(check_ptr(ws, "ws"));
   AttnDenseArgs a;
+  a.q = (const __nv_bfloat16*)g.q;
   a.q_pos = g.q_pos;
   a.kv = (const __nv_bfloat16*)g.kv_cmp;
   a.pm = pm;
@@ -1613,8 +1615,17 @@ static csa_status_t launch_attn_dense(const csa_params_t* p, const AttnArgs& g, 
   if (e != cudaSuccess) return cuda_fail(e, "k_attn_dense");
   CSA_CHECK(launched("k_attn_dense"));
   if (a.pairs == 1) return CSA_OK;  // every token is whole
-  e = launch_ex(k_attn_dense_join, dim3(4 * kApDim / kAdJoinDims, (unsigned)std::min(a.units, a.pairs)),
-                dim3(128), 0, s, 1, a);
+  // 32 warps of the join fit an SM; a unit takes 128 K of them
+  const unsigned rows = (unsigned)std::min(a.units, a.pairs);
+  const unsigned room = 32u * (unsigned)num_sms() / (128u * rows);
+  auto join = [&](auto k) {
+    constexpr int K = decltype(k)::value;
+    return launch_ex(k_attn_dense_join<K>, dim3((unsigned)(K * (kApDim / 16)), rows), dim3(128), 0, s, 1, a);
+  };
+  e = room >= 8   ? join(std::integral_constant<int, 8>{})
+      : room >= 4 ? join(std::integral_constant<int, 4>{})
+      : room >= 2 ? join(std::integral_constant<int, 2>{})
+                  : join(std::integral_constant<int, 1>{});
   if (e != cudaSuccess) return cuda_fail(e, "k_attn_dense_join");
   return launched("k_attn_dense_join");
 }
