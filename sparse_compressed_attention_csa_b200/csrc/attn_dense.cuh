@@ -303,26 +303,21 @@ __global__ void __launch_bounds__(kAdThreads, 1)
         sm.sn[head] = s;
       }
       asm volatile("bar.sync 1, 128;" ::: "memory");
-      auto rotate = [&](uint32_t (&w)[32], int d0) {  // 64 dims from d0
+      // 8 dims from d of this thread's head, turned where they rotate (small
+      // loops below: code that runs once per token is paid for in instruction
+      // fetches)
+      auto turn8 = [&](uint4 v, int d) -> uint4 {
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        if (d >= rope0) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const int d = d0 + 2 * e;
-          if (d >= rope0) {
-            const int i = (d - rope0) >> 1;
+          for (int e = 0; e < 4; ++e) {
+            const int i = ((d - rope0) >> 1) + e;
+            const float c = sm.cs[i], sn = sm.sn[i];
             const float2 f = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&w[e]));
-            w[e] = ap_bf16x2(f.x * sm.cs[i] - f.y * sm.sn[i], f.x * sm.sn[i] + f.y * sm.cs[i]);
+            w[e] = ap_bf16x2(f.x * c - f.y * sn, f.x * sn + f.y * c);
           }
         }
-      };
-      auto load64 = [&](const uint8_t* blk, uint32_t (&w)[32]) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint4 v = *reinterpret_cast<const uint4*>(blk + ap_swz(head, k));
-          w[4 * k] = v.x;
-          w[4 * k + 1] = v.y;
-          w[4 * k + 2] = v.z;
-          w[4 * k + 3] = v.w;
-        }
+        return make_uint4(w[0] ^ a.flip, w[1] ^ a.flip, w[2] ^ a.flip, w[3] ^ a.flip);
       };
       if (seg > 0)  // every QK of the last segment has read Q
         ok = __all_sync(0xffffffffu, mbar_wait_fast(&sm.q_free, (uint32_t)(seg - 1) & 1u, abortp, wait_ns));
@@ -333,39 +328,45 @@ __global__ void __launch_bounds__(kAdThreads, 1)
         ok = __all_sync(0xffffffffu, mbar_wait_fast(&sm.full[slot], (uint32_t)((item + half) / kAdSlots) & 1u,
                                                abortp, wait_ns));
         if (!ok) break;
+        const uint8_t* blk = ring + slot * kAdSlotBytes;
 #pragma unroll 1
         for (int c = 0; c < 2; ++c) {
-          uint32_t w[32], r16[16];
-          load64(ring + slot * kAdSlotBytes + c * kAdQChunk, w);
-          const int d0 = dim0 + half * 128 + c * 64;
-          if (d0 + 64 > rope0) rotate(w, d0);
+          uint4 v[8];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) w[e] ^= a.flip;
+          for (int k = 0; k < 8; ++k) v[k] = *reinterpret_cast<const uint4*>(blk + c * kAdQChunk + ap_swz(head, k));
+          const int d = dim0 + half * 128 + c * 64;
+          if (d + 64 > rope0 || a.flip != 0u) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) r16[e] = w[e];
-          tmem_st16(t_q + lane_base + (uint32_t)(half * 64 + c * 32), r16);
+            for (int k = 0; k < 8; ++k) v[k] = turn8(v[k], d + k * 8);
+          }
+          uint32_t r[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) r16[e] = w[16 + e];
-          tmem_st16(t_q + lane_base + (uint32_t)(half * 64 + c * 32 + 16), r16);
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              r[4 * k] = v[4 * h + k].x;
+              r[4 * k + 1] = v[4 * h + k].y;
+              r[4 * k + 2] = v[4 * h + k].z;
+              r[4 * k + 3] = v[4 * h + k].w;
+            }
+            tmem_st16(t_q + lane_base + (uint32_t)(half * 64 + c * 32 + h * 16), r);
+          }
         }
       }
       if (ok && (a.flip != 0u || (other0 + kApHalf > rope0 && a.rope_dim > 0))) {
         ok = __all_sync(0xffffffffu, mbar_wait_fast(&sm.q_full, (uint32_t)seg & 1u, abortp, wait_ns));
         if (ok) {
+          const int k0 = a.flip != 0u ? 0 : max(0, rope0 - other0) >> 3;
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            const int d0 = other0 + c * 64;
-            if (d0 + 64 <= rope0 && a.flip == 0u) continue;
-            uint8_t* blk = q_smem + c * kAdQChunk;
-            uint32_t w[32];
-            load64(blk, w);
-            if (d0 + 64 > rope0) rotate(w, d0);
+          for (int k = k0; k < 32; k += 4) {  // (rope0 is a multiple of 32)
+            uint4 v[4];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) w[e] ^= a.flip;
+            for (int e = 0; e < 4; ++e)
+              v[e] = *reinterpret_cast<const uint4*>(q_smem + (k >> 3) * kAdQChunk + ap_swz(head, (k & 7) + e));
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              *reinterpret_cast<uint4*>(blk + ap_swz(head, k)) =
-                  make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+            for (int e = 0; e < 4; ++e)
+              *reinterpret_cast<uint4*>(q_smem + (k >> 3) * kAdQChunk + ap_swz(head, (k & 7) + e)) =
+                  turn8(v[e], other0 + (k + e) * 8);
           }
         }
       }
