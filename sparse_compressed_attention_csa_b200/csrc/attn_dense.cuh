@@ -622,6 +622,9 @@ __global__ void __launch_bounds__(kAdThreads, 1)
                       ? a.pm.table[(long long)x.b * a.pm.width + (ix[c] >> a.pm.shift)] : -1;
       };
       int ix0[4], ix1[4], ix2[4], pg0[4], pg1[4];
+      // dense: the page table by windows, so that a whole tile waits for no load
+      PageWindow pw;
+      if (!kSparse && x.n_sel > 0) pw.start(a.pm, x.b, x.n_sel, max(0, tb - x.win_tiles) * kAdTile >> a.pm.shift);
       if (kSparse) {
         load_idx(tb, ix0);
         load_idx(tb + 1, ix1);
@@ -673,8 +676,13 @@ __global__ void __launch_bounds__(kAdThreads, 1)
           if (whole) {
             if (win)
               box = lane == 0 ? (long long)x.raw_row + (long long)i * kAdTile : -1;
-            else if (lane < subs)
-              box = page_row(a.pm, x.b, a.n_max, j0 + lane * a.box_rows);
+            else {
+              pw.seek(j0 >> a.pm.shift);
+              const int j = j0 + lane * a.box_rows;
+              const int pg = pw.at(j >> a.pm.shift);
+              if (lane < subs && (unsigned)pg < (unsigned)a.pm.n_pages)
+                box = ((long long)pg << a.pm.shift) + (j & ((1 << a.pm.shift) - 1));
+            }
             whole = __popc(__ballot_sync(0xffffffffu, box >= 0)) == (win ? 1 : subs);
           }
           vm = make_uint2(0xffffffffu, 0xffffffffu);
