@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(32 * kPgWarps) k_attn_paged_simt(const __grid_
     for (int k = 0; k < NK; ++k) qv[g][k] = to_f32(qp[32 * k]);
     pg_rotate<NK>(qv[g], a, t);
   }
-  const int n_sel = kHca ? min(n_visible(t, a.n_cmp[b], a.width, a.stride), a.n_max) : a.topk;
+  const int n_sel = kHca ? max(0, min(n_visible(t, a.n_cmp[b], a.width, a.stride), a.n_max)) : a.topk;
   const int* sel = kHca ? nullptr : a.idx + (long long)token * a.topk;
   const int rp0 = a.raw_pos0[b];
   const int w_lo = max(max(0, t - a.window + 1), rp0);

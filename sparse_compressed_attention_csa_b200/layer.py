@@ -165,6 +165,22 @@ def csa_decode_fp8(p: L.Params, q, q_pos, q_idx, w, k_idx, n_cmp, kv_cmp, cmp_sc
     return idx, out
 
 
+class _On:
+    """What a call allocates is allocated for the stream it runs on (torch's
+    allocator hands a freed block to the stream it came from)."""
+
+    def __init__(self, stream):
+        self.ctx = None if stream is None else torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
 def norm_rope(p: L.Params, q, q_weight=None, q_pos=None, k=None, k_weight=None, k_pos=None,
               k_out=None, k_slots=None, eps: float = 1e-6, stream=None):
     """RMS norm of every head of q [rows][heads][dim] (and k) and rotation of
@@ -172,9 +188,10 @@ def norm_rope(p: L.Params, q, q_weight=None, q_pos=None, k=None, k_weight=None, 
     queries and keys, token rows, or pooled entries on their way to a cache.
     Returns (q_out, k_out); with k_out and k_slots given, row r of k goes to
     row k_slots[r] of k_out."""
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if k is not None and k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    with _On(stream):
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if k is not None and k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
     L.csa_norm_rope(p, eps, q, q_weight, q_pos, q_out, k, k_weight, k_pos, k_out, k_slots, stream)
     return q_out, k_out
 
@@ -182,10 +199,11 @@ def norm_rope(p: L.Params, q, q_weight=None, q_pos=None, k=None, k_weight=None, 
 def quantize_mxfp4(rows, stream=None):
     """Rows [..., d] -> (E2M1 codes uint8 [..., d / 2], E8M0 scales uint8
     [..., d / 32]), one scale per 32 values."""
-    codes = torch.empty(rows.shape[:-1] + (rows.shape[-1] // 2,), dtype=torch.uint8,
-                        device=rows.device)
-    scales = torch.empty(rows.shape[:-1] + (rows.shape[-1] // 32,), dtype=torch.uint8,
-                         device=rows.device)
+    with _On(stream):
+        codes = torch.empty(rows.shape[:-1] + (rows.shape[-1] // 2,), dtype=torch.uint8,
+                            device=rows.device)
+        scales = torch.empty(rows.shape[:-1] + (rows.shape[-1] // 32,), dtype=torch.uint8,
+                             device=rows.device)
     L.csa_quantize_mxfp4(rows, codes, scales, stream=stream)
     return codes, scales
 
@@ -195,13 +213,15 @@ def sparse_attn_paged(p: L.Params, q, q_pos, kv_pages, page_table, idx, kv_raw, 
     """Attention over the selected entries idx [B][Tq][topk] of a paged cache
     kv_pages [n_pages][page][d] and the window's raw rows."""
     ws = ws or Workspace(q.device)
-    if out is None:
-        out = torch.empty_like(q)
     B, Tq = q_pos.shape
     nb = L._ws_bytes(p, L.CSA_OP_SPARSE_ATTN_PAGED, B, Tq, page_table.shape[1] * kv_pages.shape[1],
                      q.get_device())
-    L.csa_sparse_attn_paged(p, q, q_pos, kv_pages, page_table, idx, kv_raw, raw_pos0, n_raw, sink,
-                            out, ws.get(nb), stream)
+    with _On(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        buf = ws.get(nb)
+    L.csa_sparse_attn_paged(p, q, q_pos, kv_pages, page_table, idx, kv_raw, raw_pos0, n_raw, sink, out, buf,
+                           stream)
     return out
 
 
@@ -210,13 +230,15 @@ def hca_decode_paged(p: L.Params, q, q_pos, kv_pages, page_table, n_cmp, kv_raw,
     """HCA decode over a paged entry cache of any length; with
     Params(width=1, stride=1) every token is its own entry."""
     ws = ws or Workspace(q.device)
-    if out is None:
-        out = torch.empty_like(q)
     B, Tq = q_pos.shape
     nb = L._ws_bytes(p, L.CSA_OP_HCA_ATTN_PAGED, B, Tq, page_table.shape[1] * kv_pages.shape[1],
                      q.get_device())
-    L.hca_attn_paged(p, q, q_pos, kv_pages, page_table, n_cmp, kv_raw, raw_pos0, n_raw, sink, out,
-                     ws.get(nb), stream)
+    with _On(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        buf = ws.get(nb)
+    L.hca_attn_paged(p, q, q_pos, kv_pages, page_table, n_cmp, kv_raw, raw_pos0, n_raw, sink, out, buf,
+                    stream)
     return out
 
 
@@ -233,13 +255,15 @@ def csa_decode_paged(p: L.Params, q, q_pos, q_idx, w, k_codes, k_scales, n_cmp, 
                          f"{kv_pages.shape[1]} entries")
     ws = ws or Workspace(q.device)
     B, Tq = q_pos.shape
-    if idx is None:
-        idx = torch.empty((B, Tq, p.topk), dtype=torch.int32, device=q.device)
     q_codes, q_scales = quantize_mxfp4(q_idx, stream)
     if n_max is None:
         n_max = page_table.shape[1] * k_codes.shape[1]
     nb = L._ws_bytes(p, L.CSA_OP_INDEX_TOPK, B, Tq, n_max, q.get_device())
+    with _On(stream):
+        if idx is None:
+            idx = torch.empty((B, Tq, p.topk), dtype=torch.int32, device=q.device)
+        buf = ws.get(nb)
     L.csa_index_topk_mxfp4(p, q_codes, q_scales, w, k_codes, k_scales, page_table, q_pos, n_cmp,
-                           idx, ws.get(nb), n_max, stream)
+                           idx, buf, n_max, stream)
     return idx, sparse_attn_paged(p, q, q_pos, kv_pages, page_table, idx, kv_raw, raw_pos0, n_raw,
                                   sink, ws, out, stream)

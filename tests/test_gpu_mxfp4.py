@@ -266,3 +266,44 @@ def test_scores_repeat_on_another_stream_and_from_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(b, first)
+
+
+def test_rows_past_four_gigabytes():
+    # codes of a pool of 80M keys (5.1 GB): the last rows
+    rows = 80_000_000
+    codes = torch.empty(rows, 64, dtype=U8, device="cuda")
+    scales = torch.empty(rows, 4, dtype=U8, device="cuda")
+    x = _rows(128, 128, torch.bfloat16, 17)
+    slots = (rows - 1 - torch.arange(128, device="cuda")).to(I32)
+    csa_quantize_mxfp4(x, codes, scales, slots=slots)
+    wc, ws = oracle.mxfp4_encode(x.double().cpu().numpy())
+    np.testing.assert_array_equal(codes[-128:].flip(0).cpu().numpy(), wc)
+    # and scores of keys there, in pages of 128
+    p = Params()
+    table = torch.tensor([[rows // 128 - 1]], dtype=I32, device="cuda")
+    t, want, bound, vis = _score_case([4 * 128 + 4], 1, 64, 128, 128, 18)
+    codes.view(-1, 128, 64)[-1] = t["k_codes"][t["page_table"][0, 0].long()]
+    scales.view(-1, 128, 4)[-1] = t["k_scales"][t["page_table"][0, 0].long()]
+    far = dict(t, k_codes=codes.view(-1, 128, 64), k_scales=scales.view(-1, 128, 4), page_table=table)
+    _check_scores(p, far, want, bound, vis, 128)
+
+
+def test_scores_with_no_keys():
+    p = Params()
+    t, _, _, _ = _score_case([40, 40], 1, 64, 128, 64, 19)
+    scores = torch.full((2, 1, 16), 5.0, device="cuda")
+    none = dict(t, n_cmp=torch.tensor([-2, 0], dtype=I32, device="cuda"))
+    csa_index_scores_mxfp4(p, none["q_codes"], none["q_scales"], none["w"], none["k_codes"], none["k_scales"],
+                           none["page_table"], none["q_pos"], none["n_cmp"], scores)
+    assert torch.all(scores == 5.0)
+    csa_index_scores_mxfp4(p, t["q_codes"], t["q_scales"], t["w"], t["k_codes"], t["k_scales"],
+                           t["page_table"], t["q_pos"], t["n_cmp"], torch.empty(2, 1, 0, device="cuda"))
+    csa_poll_device_error()
+
+
+@pytest.mark.parametrize("B", [147, 149, 513])
+def test_batches_around_the_number_of_sms_and_the_plan(B):
+    p = Params()
+    lens = [40 + 37 * (i % 29) for i in range(B)]
+    t, want, bound, vis = _score_case(lens, 1, 64, 128, 64, B)
+    _check_scores(p, t, want, bound, vis, max(len(x[0]) for x in want))

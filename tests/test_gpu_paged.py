@@ -243,6 +243,97 @@ def test_results_repeat_in_place_on_streams_and_from_two_graphs():
     csa_poll_device_error()
 
 
+def test_no_pages_and_negative_counts():
+    # an empty pool and table: the window and the sink alone; then nothing at all
+    p, t, _ = _case("bf16", 128, 512, 64, [300, 7], 1, 64, 128, 128, 128, 78)
+    f = lambda a: a.double().cpu().numpy()  # noqa: E731
+    want = [oracle.hca_attn(f(t["q"][b]), t["q_pos"][b].cpu().numpy(), np.zeros((0, 512)), 0, f(t["raw"][b]),
+                            int(t["pos0"][b]), int(t["n_raw"][b]), t["sink"].cpu().numpy(), 1 / np.sqrt(512), 128,
+                            128, 128, 64, 1e4) for b in range(2)]
+    empty = dict(t, kv=t["kv"][:0], table=t["table"][:, :0].contiguous())
+    assert_close(host64(_hca(p, empty)), np.stack(want), "bf16", "no pages")
+    idx = torch.full((2, 1, 1), -1, dtype=I32, device="cuda")
+    assert_close(host64(_sparse(p, dict(empty, idx=idx))), np.stack(want), "bf16", "no pages, selection")
+    for dt in (torch.bfloat16, torch.float32):
+        u = {k: (v.to(dt) if v.dtype == torch.bfloat16 else v) for k, v in t.items()}
+        u["n_cmp"] = torch.full_like(t["n_cmp"], -3)
+        u["n_raw"] = torch.full_like(t["n_raw"], -1)
+        assert torch.all(_hca(p, u) == 0)
+    csa_poll_device_error()
+
+
+def test_another_token_with_nan_queries_and_fewer_heads_than_a_tile():
+    # the matrix tile of a 16-head token reaches into the next tokens' queries
+    p, t, want = _case("bf16", 16, 512, 64, [900, 800, 700], 1, 64, 1, 1, 64, 79)
+    t["q"][1] = float("nan")
+    out = _hca(p, t)
+    assert torch.isnan(out[1]).all()
+    assert_close(host64(out)[[0, 2]], want[[0, 2]], "bf16", "the other tokens")
+
+
+def test_the_same_entry_twice_counts_twice():
+    p, t, _ = _case("bf16", 128, 512, 64, [2000], 1, 64, 8, 4, 16, 80, topk=100)
+    t["idx"][0, 0, 50:] = t["idx"][0, 0, :50].flip(0)
+    t["idx"][0, 0, 10] = -1                              # unused places anywhere
+    f = lambda a: a.double().cpu().numpy()  # noqa: E731
+    n = int(t["n_cmp"][0])
+    want = oracle.sparse_attn(f(t["q"][0]), t["q_pos"][0].cpu().numpy(),
+                              oracle.paged_rows(t["kv"].float().cpu().numpy(), t["table"][0].cpu().numpy(), n),
+                              t["idx"][0].cpu().numpy(), f(t["raw"][0]), int(t["pos0"][0]), int(t["n_raw"][0]),
+                              t["sink"].cpu().numpy(), 1 / np.sqrt(512), 16, 64, 1e4)
+    assert_close(host64(_sparse(p, t))[0], want, "bf16", "duplicates")
+
+
+@pytest.mark.parametrize("sparse", [False, True])
+def test_pages_past_four_gigabytes(sparse):
+    # a pool of 5.2 GB whose used pages are its last: element offsets past 2^31
+    p, t, want = _case("bf16", 128, 512, 64, [3000], 1, 64, 8, 4, 128, 81, topk=256 if sparse else 0)
+    total, used = 80000, t["kv"].shape[0]
+    pool = torch.empty((total, 64, 512), dtype=torch.bfloat16, device="cuda")
+    pool[total - used:] = t["kv"]
+    live = t["table"] < used
+    t["table"][live] += total - used
+    big = dict(t, kv=pool)
+    out = _sparse(p, big) if sparse else _hca(p, big)
+    assert_close(host64(out), want, "bf16", "far pages")
+    csa_poll_device_error()
+
+
+def test_calls_on_a_given_stream_allocate_for_it():
+    p, t, want = _case("bf16", 128, 512, 64, [4000, 41], 1, 64, 8, 4, 128, 82, topk=128)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    outs = []
+    for _ in range(8):                                   # results held, workspaces freed at once
+        outs.append(_sparse(p, t, stream=side))
+        torch.empty(1 << 22, device="cuda").fill_(7.0)   # another stream's use of freed memory
+    side.synchronize()
+    assert_close(host64(outs[0]), want, "bf16", "side stream")
+    assert all(torch.equal(o, outs[0]) for o in outs)
+
+
+def test_waits_that_run_out_end_the_call_and_the_next_one_is_right():
+    # a limit of 1 ns: a wait that is not over at its first try gives up; every
+    # role winds down within its bounded drains
+    from sparse_compressed_attention_csa_b200 import csa_set_wait_limit_ns
+    p, t, want = _case("bf16", 128, 512, 64, [9000, 4000], 1, 64, 1, 1, 128, 83)
+    _hca(p, t)
+    torch.cuda.synchronize()
+    csa_set_wait_limit_ns(1)
+    try:
+        _hca(p, t)
+        torch.cuda.synchronize()
+        try:
+            csa_poll_device_error()
+        except CsaError as e:
+            assert e.status == 7
+    finally:
+        csa_set_wait_limit_ns(0)
+    out = _hca(p, t)
+    csa_poll_device_error()
+    assert_close(host64(out), want, "bf16", "after a failed launch")
+
+
 def test_workspace_too_small_is_refused():
     p, t, _ = _case("bf16", 128, 512, 64, [9000], 1, 64, 1, 1, 0, 75)
     nb = csa_workspace_size(p, CSA_OP_HCA_ATTN_PAGED, 1, 1, t["table"].shape[1] * 64)
