@@ -1256,7 +1256,7 @@ CSA_API csa_status_t csa_norm_rope(const csa_params_t* p, csa_dtype_t dtype, int
     // more when there is enough work to fill the GPU several times over
     sd.hpg = 1;
     const long long work = (long long)sd.rows * sd.heads;
-    while (sd.hpg < 8 && 2 * sd.hpg <= sd.heads && work / (2 * sd.hpg) >= 16LL * num_sms() * gpc)
+    while (sd.hpg < 32 && 2 * sd.hpg <= sd.heads && work / (2 * sd.hpg) >= 16LL * num_sms() * gpc)
       sd.hpg *= 2;
     sd.hgroups = (sd.heads + sd.hpg - 1) / sd.hpg;
     const long long blocks = ((long long)sd.rows * sd.hgroups + gpc - 1) / gpc;
@@ -1312,15 +1312,22 @@ CSA_API csa_status_t csa_quantize_mxfp4(csa_dtype_t dtype, const void* rows, int
   const long long per = (1LL << 30) / cpr;
   for (long long i0 = 0; i0 < n; i0 += per) {
     const unsigned m = (unsigned)std::min<long long>(per, n - i0);
-    const unsigned ctas = (unsigned)(((long long)m * cpr + kMxThreads - 1) / kMxThreads);
+    // two chunks a thread once there are enough to fill the GPU twice over: more
+    // bytes in flight
+    const long long chunks = (long long)m * cpr;
+    const int per_thread = chunks >= 4LL * num_sms() * 2048 ? 2 : 1;
+    const unsigned ctas = (unsigned)((chunks + kMxThreads * per_thread - 1) / (kMxThreads * per_thread));
+    auto launch = [&](auto zero, auto per) {
+      using T = decltype(zero);
+      k_quantize_mxfp4<T, decltype(per)::value><<<ctas, kMxThreads, 0, s>>>(
+          (const T*)rows + i0 * row_stride, row_stride, m, cpr, slots, i0, out_rows, codes, scales, (T*)values);
+    };
+    using One = std::integral_constant<int, 1>;
+    using Two = std::integral_constant<int, 2>;
     if (dtype == CSA_BF16)
-      k_quantize_mxfp4<__nv_bfloat16><<<ctas, kMxThreads, 0, s>>>(
-          (const __nv_bfloat16*)rows + i0 * row_stride, row_stride, m, cpr, slots, i0, out_rows,
-          codes, scales, (__nv_bfloat16*)values);
+      per_thread == 2 ? launch(__nv_bfloat16(), Two{}) : launch(__nv_bfloat16(), One{});
     else
-      k_quantize_mxfp4<float><<<ctas, kMxThreads, 0, s>>>((const float*)rows + i0 * row_stride,
-                                                          row_stride, m, cpr, slots, i0, out_rows,
-                                                          codes, scales, (float*)values);
+      per_thread == 2 ? launch(0.f, Two{}) : launch(0.f, One{});
     CSA_CHECK(launched("k_quantize_mxfp4"));
   }
   return CSA_OK;

@@ -67,63 +67,85 @@ __device__ __forceinline__ float mx_scale(int byte) {
   return __int_as_float(byte == 0 ? 0x00400000 : byte << 23);
 }
 
+__device__ __forceinline__ void mx_store8(__nv_bfloat16* p, const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+    w[k] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void mx_store8(float* p, const float (&v)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
 // Rows [0, n) of d values (row i at rows + i * row_stride) to the codes and
 // scales of row slots[i] (i without slots); `values` (nullable) receives the
 // values that the codes stand for, row i dense.  i0: first row of this launch.
-template <typename T>
+template <typename T, int PER>
 __global__ void __launch_bounds__(kMxThreads)
     k_quantize_mxfp4(const T* __restrict__ rows, long long row_stride, unsigned n, unsigned cpr,
                      const int32_t* __restrict__ slots, long long i0, long long out_rows,
                      uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
                      T* __restrict__ values) {
-  const unsigned chunk = blockIdx.x * kMxThreads + threadIdx.x;  // 8 values
-  const unsigned r = chunk / cpr, k = chunk - r * cpr;
-  const bool live = r < n;  // the four lanes of a block agree: cpr is a multiple of 4
-  float v[8];
+  unsigned r[PER], k[PER];
+  int slot[PER];
+  float v[PER][8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = 0.f;
-  if (live) load8(rows + (long long)r * row_stride + 8 * k, v);
-  // the largest magnitude as an integer: NaN and infinity sort above all
-  uint32_t top = 0;
+  for (int p = 0; p < PER; ++p) {  // PER chunks of 8 values, all loads first
+    const unsigned chunk = (blockIdx.x * PER + p) * kMxThreads + threadIdx.x;
+    r[p] = chunk / cpr;
+    k[p] = chunk - r[p] * cpr;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  if (!live) return;
-  const int field = (int)(top >> 23);
-  const bool bad = field == 255;
-  const int byte = top == 0 ? 127 : (bad ? kMxNaN : max(field - 2, 0));
-  const float inv = bad ? 0.f : __int_as_float((254 - byte) << 23);  // 1 / scale
-  uint32_t c = 0;
-  if (!bad) {
-    float q[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) q[e] = v[e] * inv;
-    c = mx_pack8(q);
-  }
-  if (values != nullptr) {
-    float q[8];
-    mx_unpack8(c, q);
-    const float s = mx_scale(byte);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) q[e] *= s;
-    T* dst = values + (i0 + r) * (long long)cpr * 8 + 8 * k;
-    store2(dst, q[0], q[1]);
-    store2(dst + 2, q[2], q[3]);
-    store2(dst + 4, q[4], q[5]);
-    store2(dst + 6, q[6], q[7]);
-  }
-  long long o = i0 + r;
-  if (slots != nullptr) {
-    const int slot = slots[i0 + r];
-    if (slot < 0 || slot >= out_rows) {
-      if (slot != -1 && k == 0) report_error(CSA_ERR_DEVICE_BOUNDS);
-      return;
+    for (int e = 0; e < 8; ++e) v[p][e] = 0.f;
+    slot[p] = 0;
+    if (r[p] < n) {
+      load8(rows + (long long)r[p] * row_stride + 8 * k[p], v[p]);
+      if (slots != nullptr) slot[p] = slots[i0 + r[p]];
     }
-    o = slot;
   }
-  reinterpret_cast<uint32_t*>(codes)[o * cpr + k] = c;
-  if ((k & 3) == 0) scales[o * (cpr >> 2) + (k >> 2)] = (uint8_t)byte;
+#pragma unroll
+  for (int p = 0; p < PER; ++p) {
+    // the largest magnitude as an integer: NaN and infinity sort above all
+    uint32_t top = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[p][e]) & 0x7fffffffu);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    if (r[p] >= n) continue;  // the four lanes of a block agree: cpr is a multiple of 4
+    const int field = (int)(top >> 23);
+    const bool bad = field == 255;
+    const int byte = top == 0 ? 127 : (bad ? kMxNaN : max(field - 2, 0));
+    const float inv = bad ? 0.f : __int_as_float((254 - byte) << 23);  // 1 / scale
+    uint32_t c = 0;
+    if (!bad) {
+      float q[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) q[e] = v[p][e] * inv;
+      c = mx_pack8(q);
+    }
+    const long long row = i0 + r[p];
+    if (values != nullptr) {
+      float q[8];
+      mx_unpack8(c, q);
+      const float s = mx_scale(byte);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) q[e] *= s;
+      mx_store8(values + row * (long long)cpr * 8 + 8 * k[p], q);
+    }
+    long long o = row;
+    if (slots != nullptr) {
+      if (slot[p] < 0 || slot[p] >= out_rows) {
+        if (slot[p] != -1 && k[p] == 0) report_error(CSA_ERR_DEVICE_BOUNDS);
+        continue;
+      }
+      o = slot[p];
+    }
+    reinterpret_cast<uint32_t*>(codes)[o * cpr + k[p]] = c;
+    if ((k[p] & 3) == 0) scales[o * (cpr >> 2) + (k[p] >> 2)] = (uint8_t)byte;
+  }
 }
 
 // ---------------------------------------------------------------------------

@@ -50,6 +50,7 @@ def _case(rows, heads, dim, dtype, seed, max_pos=1 << 20):
     (1, 1, 128, 64), (32, 64, 128, 64), (7, 5, 96, 32), (3, 128, 512, 64), (130, 1, 512, 64),
     (5, 3, 8, 8), (9, 2, 64, 0), (2, 17, 1024, 128), (70, 3, 72, 8), (1, 300, 24, 24),
     (400, 24, 256, 64), (3, 2, 512, 512),
+    (3001, 33, 128, 64), (1200, 70, 512, 64),        # several heads per lane group
 ])
 def test_queries(rows, heads, dim, rope, dtype):
     p = Params(d=1024, rope_dim=rope) if rope in (0, 32, 64, 128, 512) else Params(d=64, rope_dim=64)
