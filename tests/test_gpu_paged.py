@@ -262,6 +262,39 @@ def test_no_pages_and_negative_counts():
     csa_poll_device_error()
 
 
+def test_padded_batch_and_no_raw_rows():
+    # a padding row of a batch (position -1) gives zeros, the others their own;
+    # a cache without raw rows has no window
+    p, t, want = _case("bf16", 128, 512, 64, [600, 500, 2000], 1, 64, 1, 1, 128, 84)
+    t["q_pos"][1] = -1
+    out = _hca(p, t)
+    assert torch.all(out[1] == 0)
+    assert_close(host64(out)[[0, 2]], want[[0, 2]], "bf16", "beside padding")
+    p0, t0, want0 = _case("bf16", 128, 512, 64, [600, 70], 1, 64, 1, 1, 0, 85)
+    none = dict(t0, raw=t0["raw"][:, :0].contiguous(), n_raw=torch.zeros_like(t0["n_raw"]))
+    assert_close(host64(_hca(Params(width=1, stride=1), none)), want0, "bf16", "no raw rows")
+    csa_poll_device_error()
+
+
+def test_two_calls_at_once_on_two_streams():
+    a = _case("bf16", 128, 512, 64, [20000, 300], 1, 64, 1, 1, 128, 86)
+    b = _case("bf16", 128, 512, 64, [9000, 4000, 50], 1, 64, 8, 4, 128, 87, topk=512)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(4):
+        with torch.cuda.stream(streams[0]):
+            x = _hca(a[0], a[1])
+        with torch.cuda.stream(streams[1]):
+            y = _sparse(b[0], b[1])
+        outs.append((x, y))
+    torch.cuda.synchronize()
+    for x, y in outs:
+        assert torch.equal(x, outs[0][0]) and torch.equal(y, outs[0][1])
+    assert_close(host64(outs[0][0]), a[2], "bf16", "one stream")
+    assert_close(host64(outs[0][1]), b[2], "bf16", "the other")
+
+
 def test_another_token_with_nan_queries_and_fewer_heads_than_a_tile():
     # the matrix tile of a 16-head token reaches into the next tokens' queries
     p, t, want = _case("bf16", 16, 512, 64, [900, 800, 700], 1, 64, 1, 1, 64, 79)
