@@ -17,8 +17,13 @@
 //
 // Computing S twice costs half as much matrix work again, and the rows are
 // read twice from L2 (once from HBM), but the CTAs never wait for each other:
-// swapping partial logits, as the selected-entry kernel does, costs about
-// 1.2 us per 64 rows here, more than the second S.
+// swapping partial logits, as k_attn_pair does, costs about 1.2 us per 64 rows
+// here, more than the second S.  What bounds it: per 64 rows a CTA has 1,790
+// clocks of MMAs (16 x 48 with A in shared memory, 16 x 32 with A in TMEM, N =
+// 64; 4 x 128, N = 256) and 224 KB through shared memory (1,750 clocks); it
+// takes about 2,500.  8 ragged sequences of up to 64K rows: 91 us; 16 x 1,152
+// rows: 25 us; 32 x 1,152 selected rows: 33.5 us (42 on k_attn_pair with paged
+// rows), of which about 6 us pass before the first MMA and 8 in the join.
 //
 // TMEM (512 columns): O [0,256) | S [256,384) two buffers | Q of the own dims
 // as bf16 pairs [384,512).  Q of the other dims stays in shared memory (64
@@ -44,8 +49,10 @@
 // Where that leaves a pair more than kAdSegTiles tiles above the mean, and
 // with more tokens than pairs, the sequence is cut into equal ranges instead,
 // and a pair goes from token to token.  A token that one pair holds whole is
-// finished there; the others' parts (O / l in fp16 with a power-of-two scale
-// per head, m and l in fp32) are joined by k_attn_dense_join in their order.
+// finished there; the others' parts are joined by k_attn_dense_join in their
+// order: m and l in fp32, O / l in fp16 under a power-of-two scale per head (11
+// bits where the bf16 output keeps 8; half the bytes of fp32, which at 2 parts
+// per token is what the join spends its time on).
 #pragma once
 #include "attn_pair.cuh"
 #include "common.cuh"
@@ -60,6 +67,9 @@ constexpr int kAdSlotBytes = 32768;    // 64 rows x 256 dims, or 128 heads x 128
 constexpr int kAdChunk = 8192;         // 64 rows x 64 dims
 constexpr int kAdQChunk = 16384;       // 128 heads x 64 dims
 constexpr int kAdThreads = 320;
+// tiles that a prefetch to L2 runs ahead (8 ragged sequences to 64K rows: none
+// 94.6 us, 2 tiles 91.4, 4 tiles 92.3, 6 tiles 92.9)
+constexpr int kAdAhead = 2;
 constexpr int kAdMasks = 8;            // more tiles than the ring lets the fetch run ahead
 constexpr int kAdSegTiles = 3;         // what changing tokens costs a pair, in tiles
 constexpr int kAdMaxPairs = 128;       // units a one-token-per-pair plan may hold
@@ -682,6 +692,18 @@ __global__ void __launch_bounds__(kAdThreads, 1)
               const int pg = pw.at(j >> a.pm.shift);
               if (lane < subs && (unsigned)pg < (unsigned)a.pm.n_pages)
                 box = ((long long)pg << a.pm.shift) + (j & ((1 << a.pm.shift) - 1));
+              // a tile a few ahead on its way to L2, by one of the pair's CTAs in
+              // turn (within the window of the table at hand)
+              const int ja = j + kAdAhead * kAdTile;
+              if (q == 0 && ((i ^ part) & 1) == 0 &&
+                  (j0 + kAdAhead * kAdTile) >> (a.pm.shift + 5) == pw.w) {
+                const int pa = pw.at(ja >> a.pm.shift);
+                if (lane < subs && ja < x.n_sel && i + kAdAhead < te &&
+                    (unsigned)pa < (unsigned)a.pm.n_pages)
+                  prefetch_l2(a.kv + (((long long)pa << a.pm.shift) +
+                                      (ja & ((1 << a.pm.shift) - 1))) * kApDim,
+                              (uint32_t)a.box_rows * kApDim * 2);
+              }
             }
             whole = __popc(__ballot_sync(0xffffffffu, box >= 0)) == (win ? 1 : subs);
           }

@@ -1253,7 +1253,8 @@ CSA_API csa_status_t csa_norm_rope(const csa_params_t* p, csa_dtype_t dtype, int
       continue;
     }
     // heads per group: one while the rows are few (every row its own lanes),
-    // more when there is enough work to fill the GPU several times over
+    // up to 32 while the groups fill the GPU 16 times over (norm_rope.cuh has
+    // what either measured)
     sd.hpg = 1;
     const long long work = (long long)sd.rows * sd.heads;
     while (sd.hpg < 32 && 2 * sd.hpg <= sd.heads && work / (2 * sd.hpg) >= 16LL * num_sms() * gpc)

@@ -16,14 +16,16 @@
 //
 // Quantizer: HBM-bound.  A lane takes 8 values (16 bytes of bf16, 32 of
 // fp32), four neighbouring lanes a block: two shuffles give the block's
-// maximum, one conversion instruction packs each pair of values.
+// maximum, one conversion instruction packs each pair of values.  524,256 keys
+// of 128 in bf16 into random rows, values written too: 63 us, 4.8 TB/s, 74% of
+// the copy rate; two such pieces per thread (66.5 us with one, 78 with four).
+// The rest is the 4-byte scale rows, each a part of a 32-byte sector.
 #pragma once
 #include "common.cuh"
 #include "quantize.cuh"
 
 namespace csa {
 
-constexpr int kMxBlock = 32;
 constexpr int kMxThreads = 256;
 constexpr int kMxNaN = 255;
 
