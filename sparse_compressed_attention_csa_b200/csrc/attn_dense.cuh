@@ -22,8 +22,8 @@
 // clocks of MMAs (16 x 48 with A in shared memory, 16 x 32 with A in TMEM, N =
 // 64; 4 x 128, N = 256) and 224 KB through shared memory (1,750 clocks); it
 // takes about 2,500.  8 ragged sequences of up to 64K rows: 91 us; 16 x 1,152
-// rows: 25 us; 32 x 1,152 selected rows: 33.5 us (42 on k_attn_pair with paged
-// rows), of which about 6 us pass before the first MMA and 8 in the join.
+// rows: 21.6 us; 32 x 1,152 selected rows: 27.2 us (42 on k_attn_pair with paged
+// rows): about 5 us before the first MMA, 1.35 a tile, 5 to join the parts.
 //
 // TMEM (512 columns): O [0,256) | S [256,384) two buffers | Q of the own dims
 // as bf16 pairs [384,512).  Q of the other dims stays in shared memory (64
@@ -43,9 +43,19 @@
 // The first fetching warp leaves each tile's valid rows as a mask for the
 // softmax.
 //
-// Split: all tiles (64 rows; a token's window tiles, then its entries') form
-// one sequence.  With no more tokens than CTA pairs each pair takes part of
-// ONE token: the fewest tiles L per pair for which sum ceil(tiles / L) fits.
+// Split, few tokens: every token gets the same number of pairs, four to one, in
+// one cluster, as many as fit the GPU at once, while none takes more than
+// kAdFixedTiles tiles above an even share.  A pair knows its tiles from its own
+// token's counts, and the cluster joins its parts: each CTA sends the others
+// their share of its dims in fp32, with m and l, into their free rings, and
+// finishes its own.  32 x 1,152 selected rows 31.1 -> 27.2 us (two pairs), 16 x
+// 1,152 rows 23.1 -> 21.6 us (three) against the ranges below.  The exchange is
+// 5 us of it: 2.3 for 64 KB a CTA through distributed shared memory (15 bytes a
+// clock), 2.7 to add, turn and write; its two barriers 0.2.
+//
+// Else all tiles (64 rows; a token's window tiles, then its entries') form one
+// sequence.  With no more tokens than CTA pairs each pair takes part of ONE
+// token: the fewest tiles L per pair for which sum ceil(tiles / L) fits.
 // Where that leaves a pair more than kAdSegTiles tiles above the mean, and
 // with more tokens than pairs, the sequence is cut into equal ranges instead,
 // and a pair goes from token to token.  A token that one pair holds whole is
@@ -72,6 +82,7 @@ constexpr int kAdThreads = 320;
 constexpr int kAdAhead = 2;
 constexpr int kAdMasks = 8;            // more tiles than the ring lets the fetch run ahead
 constexpr int kAdSegTiles = 3;         // what changing tokens costs a pair, in tiles
+constexpr int kAdFixedTiles = 6;       // what the device's ranges and the join cost, in tiles
 constexpr int kAdMaxPairs = 128;       // units a one-token-per-pair plan may hold
 constexpr size_t kAdPartHalfs = 2 * (size_t)kApHeads * kApHalf;  // fp16 values of one part
 constexpr int kAdMl = 3 * kApHeads;    // m, l, scale per CTA of a part
@@ -91,6 +102,7 @@ struct AttnDenseArgs {
   int raw_max;
   const float* sink;
   int Tq, H, groups, units;  // unit: (token, group of 128 heads)
+  int fixed;  // pairs per unit in one cluster, or 0: ranges found on the device
   int window, width, stride, rope_dim;
   int pairs, box_rows;
   float scale_log2;  // |scale| log2(e), above 0
@@ -152,6 +164,27 @@ __device__ __forceinline__ AdUnit ad_unit(const AttnDenseArgs& a, int u) {
   return x;
 }
 
+// 16 dims of a finished head, times inv: the inverse rotation at -t from dim
+// rel = 0 on (all of them or none), bf16.
+__device__ __forceinline__ void ad_store16(__nv_bfloat16* dst, int rel, const float (&o)[16], float inv,
+                                           const AdMisc& sm, bool live) {
+  uint32_t w[8];
+  if (rel < 0) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = ap_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float c = sm.cs[(rel >> 1) + e] * inv, s = sm.sn[(rel >> 1) + e] * inv;
+      w[e] = ap_bf16x2(o[2 * e] * c + o[2 * e + 1] * s, -o[2 * e] * s + o[2 * e + 1] * c);
+    }
+  }
+  if (live) {
+    *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(dst + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
 template <bool kSparse>
 __global__ void __launch_bounds__(kAdThreads, 1)
     k_attn_dense(const __grid_constant__ AttnDenseArgs a, const __grid_constant__ CUtensorMap tm_q,
@@ -205,7 +238,17 @@ __global__ void __launch_bounds__(kAdThreads, 1)
   }
 
   // ---- this pair's range of tiles
-  {
+  if (a.fixed > 0) {
+    if (threadIdx.x == 0) {
+      const int k = pair % a.fixed;
+      const int n = ad_unit<kSparse>(a, pair / a.fixed).tiles;
+      sm.u0 = pair / a.fixed;
+      sm.pre0 = 0;
+      sm.total = n;
+      sm.g0 = n * k / a.fixed;
+      sm.g1 = n * (k + 1) / a.fixed;
+    }
+  } else {
     const int per = (a.units + kAdThreads - 1) / kAdThreads;  // units per thread
     const int ua = min(a.units, (int)threadIdx.x * per), ub = min(a.units, ua + per);
     int mine = 0;
@@ -291,6 +334,7 @@ __global__ void __launch_bounds__(kAdThreads, 1)
   const int g1 = sm.g1;
   int u = sm.u0, pre = sm.pre0, g = sm.g0;
   bool ok = true;
+  float m_run = -INFINITY, l_run = 0.f;  // softmax warps: of the segment at hand
 
   if (warp < 4) {
     // ======================= softmax warps
@@ -393,7 +437,8 @@ __global__ void __launch_bounds__(kAdThreads, 1)
       item += 2 + 2 * (te - tb);
 
       // ---- the tiles
-      float m_run = -INFINITY, l_run = 0.f;
+      m_run = -INFINITY;
+      l_run = 0.f;
       const int gt0 = gt;
       for (int i = tb; i < te; ++i, ++gt) {
         const int sb = gt & 1;
@@ -485,6 +530,7 @@ __global__ void __launch_bounds__(kAdThreads, 1)
                                                abortp, wait_ns));
       ok = ap_softmax_all(ok);
       if (!ok) break;
+      if (a.fixed > 1) break;  // joined below
       tc_fence_after();
       const int h = (u % a.groups) * kApHeads + head;  // head of the token
       const bool live = h < a.H;
@@ -496,33 +542,15 @@ __global__ void __launch_bounds__(kAdThreads, 1)
         const float scl = den > 0.f || den != den ? wm / den : 0.f;
         __nv_bfloat16* orow = a.out + ((size_t)x.token * a.H + (live ? h : 0)) * kApDim + dim0;
 #pragma unroll 1
-        for (int sl = 0; sl < 8; ++sl) {
-          uint32_t r[32];
-          tmem_ld32(t_o + lane_base + (uint32_t)(sl * 32), r);
-          tmem_wait_ld();
-          float o[32];
+        for (int d = 0; d < kApHalf; d += 16) {
+          uint32_t r[2][8];
+          tmem_ld8(t_o + lane_base + (uint32_t)d, r[0]);
+          tmem_ld8(t_o + lane_base + (uint32_t)d + 8, r[1]);
+          tmem_wait_ld8(r[0], r[1]);
+          float o[16];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(r[e]) * scl;
-          const int d0 = dim0 + sl * 32;
-          if (d0 + 32 > rope0) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const int d = d0 + e;
-              if (d >= rope0) {  // inverse rotation at -t
-                const int ii = (d - rope0) >> 1;
-                const float x0 = o[e], x1 = o[e + 1];
-                o[e] = x0 * sm.cs[ii] + x1 * sm.sn[ii];
-                o[e + 1] = -x0 * sm.sn[ii] + x1 * sm.cs[ii];
-              }
-            }
-          }
-          if (live) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              *reinterpret_cast<uint4*>(orow + sl * 32 + 8 * k) = make_uint4(
-                  ap_bf16x2(o[8 * k], o[8 * k + 1]), ap_bf16x2(o[8 * k + 2], o[8 * k + 3]),
-                  ap_bf16x2(o[8 * k + 4], o[8 * k + 5]), ap_bf16x2(o[8 * k + 6], o[8 * k + 7]));
-          }
+          for (int e = 0; e < 16; ++e) o[e] = __uint_as_float(r[e >> 3][e & 7]);
+          ad_store16(orow + d, dim0 + d - rope0, o, scl, sm, live);
         }
       } else {
         // a part: O / l times a power of two that puts the head's largest
@@ -568,7 +596,7 @@ __global__ void __launch_bounds__(kAdThreads, 1)
       tc_fence_before();
       mbar_arrive(&sm.o_free);
       // the join's work list: the pair that holds a unit's first tile writes it
-      if (first && part == 0 && threadIdx.x == 0) {
+      if (a.fixed == 0 && first && part == 0 && threadIdx.x == 0) {
         // the pair of the unit's last tile: the largest p with total p / pairs <= that tile
         const int last = sm.last >= 0 ? sm.last
                                       : (int)(((long long)(pre + x.tiles) * a.pairs - 1) / sm.total);
@@ -885,6 +913,101 @@ __global__ void __launch_bounds__(kAdThreads, 1)
   }
   __syncwarp();
   tc_fence_before();
+  if (a.fixed > 1) {
+    // The unit's pairs are a cluster: each hands the others their share of its
+    // dims, in fp32 and unscaled, with m and l, and finishes its own share.
+    // Warps w and w + 4 read the same TMEM lanes and take every other 16 dims.
+    // (Small loops: this runs once, and its instructions are fetched as it goes.)
+    const int P = a.fixed, k = pair % P, unit = pair / P, head = (warp & 3) * 32 + lane, first = warp >> 2;
+    const int h = (unit % a.groups) * kApHeads + head;
+    const bool live = h < a.H && warp < 8;
+    const float sink_l2 = live ? a.sink[h] * 1.4426950408889634f : 0.f;
+    const bool have = sm.g1 > sm.g0;
+    const uint32_t t_head = t_o + ((uint32_t)((warp & 3) * 32) << 16);
+    auto share = [&](int r) { return kApHalf / 32 * r / P * 32; };  // first dim of pair r's share
+    const int piece = kApHeads * 4 * 32 * ((kApHalf / 32 + P - 1) / P);
+    uint8_t* ml = ring + (P - 1) * piece + head * 8;  // + slot * 1 KB
+    // a pair without tiles says so by l = -1
+    if (first == 0 && !have && head < a.rope_dim / 2)
+      rope_cs_reduced(a.q_pos[unit / a.groups], a.freq[head], &sm.cs[head], &sm.sn[head]);
+    cluster_sync_all();  // the rings are free: every copy and product is done
+    tc_fence_after();
+    if (warp < 8) {
+#pragma unroll 1
+      for (int j = 0; j < P; ++j) {
+        const int r = (k + 1 + j) % P;  // its slot j is this pair's; slot P - 1 this pair's own
+        if (have && j < P - 1) {
+          const int d1 = share(r + 1);
+          int d = share(r) + first * 16;
+          uint32_t dst = mapa(ring + j * piece, (uint32_t)(2 * r + part)) + (uint32_t)(first * 4 * kApHeads + head) * 16;
+#pragma unroll 1
+          for (; d < d1; d += 32, dst += 8 * kApHeads * 16) {
+            uint32_t v[2][8];
+            tmem_ld8(t_head + (uint32_t)d, v[0]);
+            tmem_ld8(t_head + (uint32_t)d + 8, v[1]);
+            tmem_wait_ld8(v[0], v[1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              st_cluster_v4(dst + (uint32_t)(e * kApHeads * 16),
+                            make_uint4(v[e >> 1][4 * (e & 1)], v[e >> 1][4 * (e & 1) + 1],
+                                       v[e >> 1][4 * (e & 1) + 2], v[e >> 1][4 * (e & 1) + 3]));
+          }
+        }
+        if (first == 0)
+          st_cluster_v2(mapa(ml + j * kApHeads * 8, (uint32_t)(2 * r + part)), __float_as_uint(m_run),
+                        __float_as_uint(have ? l_run : -1.f));
+      }
+    }
+    __syncwarp();
+    cluster_sync_all();  // the shares are here; nobody writes into a CTA that has left
+    if (warp < 8) {
+      float M = sink_l2;
+#pragma unroll 1
+      for (int j = 0; j < P; ++j) M = fmaxf(M, *reinterpret_cast<const float*>(ml + j * kApHeads * 8));
+      M = M == -INFINITY ? 0.f : M;
+      float L = ap_ex2(sink_l2 - M), w_own = 0.f;
+#pragma unroll 1
+      for (int j = 0; j < P; ++j) {
+        const float2 x = *reinterpret_cast<const float2*>(ml + j * kApHeads * 8);
+        w_own = ap_ex2(x.x - M);  // (slot P - 1 comes last)
+        if (!(x.y < 0.f)) L = fmaf(x.y, w_own, L);
+      }
+      const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+      const int d1 = share(k + 1);
+      int d = share(k) + first * 16;
+      __nv_bfloat16* dst = a.out + ((size_t)(unit / a.groups) * a.H + (live ? h : 0)) * kApDim + dim0;
+      const uint8_t* got = ring + (first * 4 * kApHeads + head) * 16;
+#pragma unroll 1
+      for (; d < d1; d += 32, got += 8 * kApHeads * 16) {
+        float o[16];
+        uint32_t v[2][8];
+        if (have) {
+          tmem_ld8(t_head + (uint32_t)d, v[0]);
+          tmem_ld8(t_head + (uint32_t)d + 8, v[1]);
+          tmem_wait_ld8(v[0], v[1]);
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] = have ? __uint_as_float(v[e >> 3][e & 7]) * w_own : 0.f;
+#pragma unroll 1
+        for (int j = 0; j < P - 1; ++j) {
+          const float2 x = *reinterpret_cast<const float2*>(ml + j * kApHeads * 8);
+          if (x.y < 0.f) continue;  // nothing was sent
+          const float w = ap_ex2(x.x - M);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float4 y = *reinterpret_cast<const float4*>(got + j * piece + e * kApHeads * 16);
+            o[4 * e] = fmaf(y.x, w, o[4 * e]);
+            o[4 * e + 1] = fmaf(y.y, w, o[4 * e + 1]);
+            o[4 * e + 2] = fmaf(y.z, w, o[4 * e + 2]);
+            o[4 * e + 3] = fmaf(y.w, w, o[4 * e + 3]);
+          }
+        }
+        ad_store16(dst + d, dim0 + d - rope0, o, inv, sm, live);
+      }
+    }
+    __syncwarp();
+    tc_fence_before();
+  }
   __syncthreads();
   if (warp == 8) {
     tc_fence_after();

@@ -514,6 +514,49 @@ DenseWs attn_dense_ws(const csa_params_t* p, bool sparse, int B, int Tq, int n_m
   return w;
 }
 
+// Clusters of `pairs` CTA pairs of the paged tensor-core kernel that fit the GPU
+// at once (asked once per device).
+template <bool kSparse>
+int attn_dense_clusters(int pairs) {
+  if (pairs == 1) return num_sms() / 2;  // needs no cluster
+  static std::atomic<int> cached[64][4];  // [device][pairs - 1], count + 1
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) return 0;
+  int n = cached[dev][pairs - 1].load(std::memory_order_relaxed) - 1;
+  if (n >= 0) return n;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * pairs));
+  cfg.blockDim = dim3(kAdThreads);
+  cfg.dynamicSmemBytes = kAdSmemBytes;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)(2 * pairs);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, k_attn_dense<kSparse>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  cached[dev][pairs - 1].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
+// Pairs per unit of a launch that gives every unit the same, in one cluster (0:
+// none does, ranges of tiles are found on the device and joined by a second
+// kernel): the most that fit the GPU at once, as long as the longest unit takes
+// no more than kAdFixedTiles tiles per pair above an even share.  Entries to
+// attend are topk for every selecting token; of a dense cache the host knows
+// only the most, so an even share counts as nothing there.
+template <bool kSparse>
+int attn_dense_fixed(long long units, long long tiles, int pairs) {
+  const long long even = kSparse ? (units * tiles + pairs - 1) / pairs : 0;
+  for (int f = 4; f >= 1; --f)
+    if ((tiles + f - 1) / f <= even + kAdFixedTiles && units <= attn_dense_clusters<kSparse>(f)) return f;
+  return 0;
+}
+
 // Limit of every bounded device-side wait (csa_set_wait_limit_ns).
 constexpr unsigned long long kDefaultWaitNs = 2000000000ull;
 std::atomic<unsigned long long> g_wait_ns{kDefaultWaitNs};
@@ -1618,11 +1661,13 @@ static csa_status_t launch_attn_dense(const csa_params_t* p, const AttnArgs& g, 
                            (uint32_t)a.box_rows));
   CSA_CHECK(make_tmap_bf16(&tr, raw_rows ? g.kv_raw : g.q, kApDim, raw_rows ? raw_rows : q_rows, 64, kAdTile));
   CSA_CHECK(set_smem_attr(k_attn_dense<kSparse>, kAdSmemBytes, "k_attn_dense"));
-  cudaError_t e = launch_ex(k_attn_dense<kSparse>, dim3((unsigned)(2 * a.pairs)), dim3(kAdThreads), kAdSmemBytes, s, 1,
-                            a, tq, tkv, tr);
+  a.fixed = attn_dense_fixed<kSparse>(units, tiles - 1, a.pairs);
+  const int grid = 2 * (a.fixed > 0 ? a.units * a.fixed : a.pairs);
+  cudaError_t e = launch_ex(k_attn_dense<kSparse>, dim3((unsigned)grid), dim3(kAdThreads), kAdSmemBytes, s,
+                            a.fixed > 1 ? 2 * a.fixed : 1, a, tq, tkv, tr);
   if (e != cudaSuccess) return cuda_fail(e, "k_attn_dense");
   CSA_CHECK(launched("k_attn_dense"));
-  if (a.pairs == 1) return CSA_OK;  // every token is whole
+  if (a.fixed > 0 || a.pairs == 1) return CSA_OK;  // every token is finished
   // 32 warps of the join fit an SM; a unit takes 128 K of them
   const unsigned rows = (unsigned)std::min(a.units, a.pairs);
   const unsigned room = 32u * (unsigned)num_sms() / (128u * rows);

@@ -311,6 +311,17 @@ __device__ __forceinline__ void st_async_v4(uint32_t remote, uint4 v, uint32_t r
       : "memory");
 }
 
+// 16-byte store into another cluster CTA's shared memory (address from mapa).
+__device__ __forceinline__ void st_cluster_v4(uint32_t remote, uint4 v) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(remote), "r"(v.x), "r"(v.y),
+               "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
+__device__ __forceinline__ void st_cluster_v2(uint32_t remote, uint32_t x, uint32_t y) {
+  asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(remote), "r"(x), "r"(y) : "memory");
+}
+
 // Arrive on another cluster CTA's mbarrier, ordering this thread's earlier
 // memory accesses before it at cluster scope.
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t remote_bar) {

@@ -276,6 +276,50 @@ def test_padded_batch_and_no_raw_rows():
     csa_poll_device_error()
 
 
+@pytest.mark.parametrize("B,rope,window", [(3, 64, 128), (15, 128, 128), (18, 64, 0), (30, 128, 128), (50, 64, 128),
+                                           (74, 128, 0), (80, 64, 128)])
+@pytest.mark.parametrize("selected", [False, True])
+def test_a_token_on_one_to_four_pairs(B, rope, window, selected):
+    # short tokens in batches that leave a token four CTA pairs, three, two, one
+    # and a share of one: empty tokens, and pairs that get no tile, among them
+    rng = np.random.default_rng(B)
+    lens = [1, 0, 65] + [int(n) for n in rng.integers(0, 250, B - 3)]
+    p, t, want = _case("bf16", 128, 512, rope, lens, 1, 16, 1, 1, window, 200 + B, topk=100 if selected else 0)
+    out = (_sparse if selected else _hca)(p, t)
+    torch.cuda.synchronize()
+    csa_poll_device_error()
+    assert_close(host64(out), want, "bf16", f"{B} tokens")
+    assert torch.equal(out, (_sparse if selected else _hca)(p, t))
+
+
+@pytest.mark.parametrize("heads", [40, 256])
+def test_head_groups_on_several_pairs(heads):
+    p, t, want = _case("bf16", heads, 512, 64, [300, 90], 2, 16, 1, 1, 128, 240 + heads)
+    out = _hca(p, t)
+    torch.cuda.synchronize()
+    csa_poll_device_error()
+    assert_close(host64(out), want, "bf16", f"{heads} heads")
+
+
+def test_nan_rows_reach_their_own_token_only():
+    # one row of one pair's share; a query; a sink
+    p, t, want = _case("bf16", 128, 512, 64, [350, 340, 330, 320], 1, 16, 1, 1, 0, 260)
+    kv = t["kv"].clone()
+    page, row = int(t["table"][0, 5]), 3
+    kv[page, row] = float("nan")
+    t["kv"] = kv
+    t["q"][1, 0, 7] = float("nan")
+    t["sink"][9] = float("nan")
+    out = host64(_hca(p, t))
+    torch.cuda.synchronize()
+    csa_poll_device_error()
+    assert np.all(np.isnan(out[0])) and np.all(np.isnan(out[1, 0, 7]))
+    assert np.all(np.isnan(out[:, 0, 9]))
+    keep = np.ones(128, dtype=bool)
+    keep[[7, 9]] = False
+    assert_close(out[1:][:, :, keep], want[1:][:, :, keep], "bf16", "beside NaN")
+
+
 def test_two_calls_at_once_on_two_streams():
     a = _case("bf16", 128, 512, 64, [20000, 300], 1, 64, 1, 1, 128, 86)
     b = _case("bf16", 128, 512, 64, [9000, 4000, 50], 1, 64, 8, 4, 128, 87, topk=512)
