@@ -22,8 +22,8 @@
 // clocks of MMAs (16 x 48 with A in shared memory, 16 x 32 with A in TMEM, N =
 // 64; 4 x 128, N = 256) and 224 KB through shared memory (1,750 clocks); it
 // takes about 2,500.  8 ragged sequences of up to 64K rows: 91 us; 16 x 1,152
-// rows: 21.6 us; 32 x 1,152 selected rows: 27.2 us (42 on k_attn_pair with paged
-// rows): about 5 us before the first MMA, 1.35 a tile, 5 to join the parts.
+// rows: 21.2 us; 32 x 1,152 selected rows: 26.6 us (42 on k_attn_pair with paged
+// rows): about 4 us before the first MMA, 1.35 a tile, 5 to join the parts.
 //
 // TMEM (512 columns): O [0,256) | S [256,384) two buffers | Q of the own dims
 // as bf16 pairs [384,512).  Q of the other dims stays in shared memory (64
@@ -48,8 +48,8 @@
 // kAdFixedTiles tiles above an even share.  A pair knows its tiles from its own
 // token's counts, and the cluster joins its parts: each CTA sends the others
 // their share of its dims in fp32, with m and l, into their free rings, and
-// finishes its own.  32 x 1,152 selected rows 31.1 -> 27.2 us (two pairs), 16 x
-// 1,152 rows 23.1 -> 21.6 us (three) against the ranges below.  The exchange is
+// finishes its own.  32 x 1,152 selected rows 31.1 -> 26.6 us (two pairs), 16 x
+// 1,152 rows 23.1 -> 21.2 us (three) against the ranges below.  The exchange is
 // 5 us of it: 2.3 for 64 KB a CTA through distributed shared memory (15 bytes a
 // clock), 2.7 to add, turn and write; its two barriers 0.2.
 //
@@ -226,6 +226,11 @@ __global__ void __launch_bounds__(kAdThreads, 1)
     tmem_alloc(&sm.tmem_base, 512);
     tmem_relinquish();
   }
+  if (a.fixed > 0) {  // the barriers and TMEM are ready
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  }
   griddep_wait();  // the predecessor's writes are visible
   griddep_launch_dependents();
   if (threadIdx.x == 0) {
@@ -238,16 +243,13 @@ __global__ void __launch_bounds__(kAdThreads, 1)
   }
 
   // ---- this pair's range of tiles
-  if (a.fixed > 0) {
-    if (threadIdx.x == 0) {
-      const int k = pair % a.fixed;
-      const int n = ad_unit<kSparse>(a, pair / a.fixed).tiles;
-      sm.u0 = pair / a.fixed;
-      sm.pre0 = 0;
-      sm.total = n;
-      sm.g0 = n * k / a.fixed;
-      sm.g1 = n * (k + 1) / a.fixed;
-    }
+  int u, pre, g, g1;
+  if (a.fixed > 0) {  // every thread finds it by itself
+    u = pair / a.fixed;
+    const int n = ad_unit<kSparse>(a, u).tiles;
+    pre = 0;
+    g = n * (pair % a.fixed) / a.fixed;
+    g1 = n * (pair % a.fixed + 1) / a.fixed;
   } else {
     const int per = (a.units + kAdThreads - 1) / kAdThreads;  // units per thread
     const int ua = min(a.units, (int)threadIdx.x * per), ub = min(a.units, ua + per);
@@ -324,15 +326,18 @@ __global__ void __launch_bounds__(kAdThreads, 1)
         sm.g1 = g1;
       }
     }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    g1 = sm.g1;
+    u = sm.u0;
+    pre = sm.pre0;
+    g = sm.g0;
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
   const uint32_t t_o = tmem, t_s = tmem + 256, t_q = tmem + 384;
   volatile int* abortp = &sm.abort_flag;
-  const int g1 = sm.g1;
-  int u = sm.u0, pre = sm.pre0, g = sm.g0;
+  const bool have = g1 > g;  // any tiles
   bool ok = true;
   float m_run = -INFINITY, l_run = 0.f;  // softmax warps: of the segment at hand
 
@@ -922,7 +927,6 @@ __global__ void __launch_bounds__(kAdThreads, 1)
     const int h = (unit % a.groups) * kApHeads + head;
     const bool live = h < a.H && warp < 8;
     const float sink_l2 = live ? a.sink[h] * 1.4426950408889634f : 0.f;
-    const bool have = sm.g1 > sm.g0;
     const uint32_t t_head = t_o + ((uint32_t)((warp & 3) * 32) << 16);
     auto share = [&](int r) { return kApHalf / 32 * r / P * 32; };  // first dim of pair r's share
     const int piece = kApHeads * 4 * 32 * ((kApHalf / 32 + P - 1) / P);
