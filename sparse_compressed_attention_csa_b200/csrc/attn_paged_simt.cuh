@@ -8,7 +8,8 @@
 // in registers (2 HG d / 32 = 64 of them).  The warps' online-softmax states
 // are joined in shared memory; with one split the CTA finishes the output,
 // else it writes (m, l, acc) in fp32 and k_attn_paged_join combines the
-// splits in their order (deterministic).  Bound by its multiply-adds and by
+// splits in their order (deterministic).  A NaN logit makes l NaN, and weights
+// of 0 in the joins leave it so.  Bound by its multiply-adds and by
 // reading each row once per HG heads: 16 x 1,152 rows of 512 in bf16 under 128
 // heads took 617 us here, 25 us on the tensor-core kernel that took over d =
 // 512 in bf16 (attn_dense.cuh).
@@ -136,7 +137,8 @@ __global__ void __launch_bounds__(32 * kPgWarps) k_attn_paged_simt(const __grid_
       const float z = warp_sum(dot) * a.scale;
       const float mn = fmaxf(m[g], z);
       const float alpha = mn == -INFINITY ? 1.f : expf(m[g] - mn);
-      const float p = mn == -INFINITY ? 0.f : expf(z - mn);
+      // guarded by z itself: the maximum passes a NaN over, the sum keeps it
+      const float p = z == -INFINITY ? 0.f : expf(z - mn);
       l[g] = fmaf(l[g], alpha, p);
 #pragma unroll
       for (int k = 0; k < NK; ++k) acc[g][k] = fmaf(p, rv[k], acc[g][k] * alpha);
