@@ -366,7 +366,8 @@ csa_status_t csa_quantize_mxfp4(csa_dtype_t dtype, const void* rows, int64_t row
  *   q_codes [B][Tq][H_I][d_I / 2], q_scales [B][Tq][H_I][d_I / 32]
  *   k_codes [n_pages][page_size][d_I / 2], k_scales [n_pages][page_size]
  *           [d_I / 32], page_table [B][table_width]; or, with page_table NULL
- *           and table_width 0, contiguous keys [B][n_max][...]
+ *           and table_width 0, contiguous keys [B][n_max][...] (an empty page
+ *           table is a non-NULL one, which no n_max above 0 fits)
  *   scores  [B][Tq][n_max] fp32, n_max <= table_width * page_size; entries j
  *           >= n_visible, and entries of pages outside the pool, are not
  *           written

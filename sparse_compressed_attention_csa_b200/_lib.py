@@ -666,6 +666,10 @@ def _mx_index_args(p, q_codes, q_scales, w, k_codes, k_scales, page_table, q_pos
         width = _shape(page_table, "page_table", 2)[1]
         tab = ((page_table, "page_table", i32, (B, width)),)
         n_max = width * page if n_max is None else n_max
+        if width == 0 and n_max > 0:
+            # torch gives an empty table the address NULL, which the library
+            # takes for contiguous keys
+            raise ValueError(f"n_max={n_max} beyond an empty page table")
     a = _args(dev, (q_codes, "q_codes", u8, (B, Tq, H, D // 2)),
               (q_scales, "q_scales", u8, (B, Tq, H, D // 32)), (w, "w", torch.float32, (B, Tq, H)),
               (k_codes, "k_codes", u8, (pages, page, D // 2)),
