@@ -67,9 +67,10 @@ struct IdxMxSmem {
   alignas(16) float w[2][QU][kImHeads];
   int tiles[kImMaxPlan];
   uint64_t full[STAGES], empty[STAGES], raw_full[STAGES], acc_full[kImBufs], acc_empty[kImBufs];
-  uint64_t q_full[2], q_empty[2], mma_drain;
+  uint64_t q_full[2], q_empty[2], mma_drain, scales_over;
   uint32_t tmem_base;
   int abort_flag;
+  int scaled;  // tiles whose scales were reordered, once scales_over is complete
   int u0, pre0, g0, g1;  // planned: first unit, its first tile, the CTA's range of tiles
 };
 
@@ -150,6 +151,7 @@ __global__ void __launch_bounds__(160 + 128 * PAR, 1)
       mbar_init(&sm.q_empty[i], 4 * PAR + 1);
     }
     mbar_init(&sm.mma_drain, 1);
+    mbar_init(&sm.scales_over, 1);
     sm.abort_flag = 0;
     fence_barrier_init();
   }
@@ -267,6 +269,7 @@ __global__ void __launch_bounds__(160 + 128 * PAR, 1)
     // ---------------- key tiles, every second one
     const int turn = warp == 0 ? 0 : 1;
     if (lane == 0) tma_prefetch_desc(&tm_k);
+    static_assert(STAGES % 2 == 0, "a stage belongs to one fetching warp");
     const int subs = kImKeys / a.box_rows;  // boxes per tile, at most 32
     int n = 0;                              // tiles requested
     bool ok = true;
@@ -311,12 +314,23 @@ __global__ void __launch_bounds__(160 + 128 * PAR, 1)
         }
       }
     }
-    // every copy into shared memory lands before the CTA may exit
-    if (lane == 0 && turn == 0)
-      for (int i = max(0, n - STAGES); i < n; ++i) {
-        mbar_drain(&sm.raw_full[i % STAGES], (uint32_t)(i / STAGES) & 1u, kImDrainNs);
-        mbar_drain(&sm.full[i % STAGES], (uint32_t)(i / STAGES) & 1u, kImDrainNs);
+    // every copy into shared memory lands before the CTA may exit: each warp
+    // waits for the last tiles that it asked for itself (after a wait that ran
+    // out the other may have asked for fewer, or for more).  `full` also counts
+    // warp 3: where that left before a tile, its arrival is made up here
+    if (lane == 0) {
+      auto drain = [](uint64_t* bar, uint32_t parity) {  // (a call is worth 220 clocks)
+        return mbar_try_wait(bar, parity) || mbar_drain(bar, parity, kImDrainNs);
+      };
+      int i0 = max(0, n - STAGES);
+      i0 += (i0 & 1) != turn ? 1 : 0;
+      for (int i = i0; i < n; i += 2) drain(&sm.raw_full[i % STAGES], (uint32_t)(i / STAGES) & 1u);
+      const bool over = drain(&sm.scales_over, 0);
+      for (int i = i0; i < n; i += 2) {
+        if (over && i >= sm.scaled) mbar_arrive(&sm.full[i % STAGES]);
+        drain(&sm.full[i % STAGES], (uint32_t)(i / STAGES) & 1u);
       }
+    }
   } else if (warp == 2) {
     // ---------------- queries, their scales and weights
     if (lane == 0) tma_prefetch_desc(&tm_q);
@@ -384,6 +398,10 @@ __global__ void __launch_bounds__(160 + 128 * PAR, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.full[s]);
       }
+    }
+    if (lane == 0) {
+      sm.scaled = n;
+      mbar_arrive(&sm.scales_over);
     }
   } else if (warp == 1) {
     // ---------------- MMA issuer (the whole warp runs the loop, one elected
