@@ -449,7 +449,8 @@ csa_status_t csa_index_topk_noalloc(const csa_params_t* p, csa_dtype_t dtype, co
  * kernel winds down without finishing its output.  0 restores the default
  * of 2 s.  Process-wide, read when a kernel is launched (a captured CUDA
  * graph keeps the limit it was captured with).  A diagnostic: a tiny limit
- * makes the timeout path run on purpose. */
+ * makes the timeout path run on purpose (a wait for a copy that is about to
+ * land may still outlast it; the waits for a token's queries do not). */
 void csa_set_wait_limit_ns(uint64_t ns);
 
 /* Number of kernels this library has launched (or recorded into a stream

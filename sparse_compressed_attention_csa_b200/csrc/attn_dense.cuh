@@ -832,7 +832,8 @@ __global__ void __launch_bounds__(kAdThreads, 1)
       const AdUnit x = ad_unit<kSparse>(a, u);
       const int n = min(x.tiles, g1 - pre) - (g - pre);
       item += 2;  // Q's own dims
-      ok = wait(&sm.q_full, seg) && wait(&sm.q_ready, seg);
+      ok = wait(&sm.q_full, seg) &&
+           __all_sync(0xffffffffu, mbar_wait_strict(&sm.q_ready, (uint32_t)seg & 1u, abortp, wait_ns));
       for (int i = 0; i <= n && ok; ++i) {
         if (i < n) {  // S(i) = Q K^T
           const uint32_t d = t_s + (uint32_t)(((gt + i) & 1) * 64);

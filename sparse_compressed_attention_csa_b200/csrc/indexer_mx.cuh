@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(160 + 128 * PAR, 1)
     for (int k = 0; ok && item(k, &it); ++k) {
       if (it.te <= it.tb) continue;
       const int qb = n & 1;
-      ok = __all_sync(0xffffffffu, mbar_wait_fast(&sm.q_full[qb], (uint32_t)(n >> 1) & 1u, abortp, wait_ns));
+      ok = __all_sync(0xffffffffu, mbar_wait_strict(&sm.q_full[qb], (uint32_t)(n >> 1) & 1u, abortp, wait_ns));
       const bool paged = a.pm.table != nullptr;
       PageWindow pw;
       if (paged) pw.start(a.pm, it.b, it.nv, (it.tb * kImKeys) >> a.pm.shift);

@@ -65,6 +65,19 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// Whether the phase is complete, at once.
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // As mbar_try_wait, suspending the thread for at most `hint_ns` while the
 // phase is incomplete.
 __device__ __forceinline__ bool mbar_try_wait_for(uint64_t* bar, uint32_t parity,
@@ -94,8 +107,8 @@ __device__ __forceinline__ uint32_t suspend_hint(uint64_t limit_ns) {
 // the CTA is aborting (flag set by another thread, or a timeout recorded by
 // any CTA) or when this wait ran out (then it sets the flag and records the
 // timeout).  The clock is read after the second unsuccessful try and every
-// 64 tries, and no try suspends longer than the limit, so even a limit of a
-// few nanoseconds runs out on a phase that is not complete at once.  `site`
+// 64 tries; a try may outlast a copy whatever hint it has, so a limit of a few
+// microseconds may not run out on a phase that is about to complete.  `site`
 // (the caller's source line) is recorded with a timeout.
 __device__ __noinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                        uint64_t limit_ns = kWaitLimitNs,
@@ -123,13 +136,40 @@ __device__ __noinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile 
 // mbar_wait with its first try inline: on a phase that is complete, or
 // completes while the instruction waits, it costs about 6 clocks, where the
 // call and the suspend hint cost 220 (measured between batches of 16 MMAs,
-// which then stall for them).
+// which then stall for them).  That try suspends for as long as the hardware
+// likes, longer than most copies take: such a wait may outlast a tiny limit.
 __device__ __forceinline__ bool mbar_wait_fast(uint64_t* bar, uint32_t parity,
                                                volatile int* abort_flag,
                                                uint64_t limit_ns = kWaitLimitNs,
                                                int site = __builtin_LINE()) {
   if (mbar_try_wait(bar, parity)) return true;
   return mbar_wait(bar, parity, abort_flag, limit_ns, site);
+}
+
+// As mbar_wait, without suspending, the clock read at every test: even a limit
+// of a few nanoseconds runs out on a phase that is not complete at once.
+__device__ __noinline__ bool mbar_spin(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                       uint64_t limit_ns, int site) {
+  const uint64_t t0 = globaltimer();
+  while (!mbar_test_wait(bar, parity)) {
+    const bool out = globaltimer() - t0 > limit_ns;
+    if (!out && !*abort_flag && !timeout_recorded()) continue;
+    *abort_flag = 1;
+    if (out) report_error(CSA_ERR_DEVICE_TIMEOUT, site);
+    return false;
+  }
+  return true;
+}
+
+// mbar_wait_fast, but a limit below kMaxSuspendNs (a diagnostic) runs out when
+// it says.  For waits once per unit of work: the test of the limit costs the
+// loops over tiles 2 to 4%.
+__device__ __forceinline__ bool mbar_wait_strict(uint64_t* bar, uint32_t parity,
+                                                 volatile int* abort_flag,
+                                                 uint64_t limit_ns = kWaitLimitNs,
+                                                 int site = __builtin_LINE()) {
+  if (limit_ns < kMaxSuspendNs) return mbar_spin(bar, parity, abort_flag, limit_ns, site);
+  return mbar_wait_fast(bar, parity, abort_flag, limit_ns, site);
 }
 
 // Wind-down drain: wait, up to the limit, for a phase that copies already in
