@@ -64,6 +64,11 @@ class Params:
     rope_beta_fast: float = 32.0  # YaRN beta
     rope_beta_slow: float = 1.0   # YaRN alpha
 
+    def __getstate__(self):
+        """The fields alone: what calls keep here (the C struct, a pointer to
+        it, workspace sizes) is not copied or pickled."""
+        return {f: self.__dict__[f] for f in self.__dataclass_fields__}
+
     def c(self) -> csa_params_t:
         """The C struct, built once per (immutable) parameter set; the
         library only reads it during a call."""

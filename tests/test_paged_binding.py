@@ -59,3 +59,17 @@ def test_an_empty_page_table_is_not_contiguous_keys(recorded):
     csa.csa_index_scores_mxfp4(p, *t.values(), torch.zeros(3, 1, 40))
     args = recorded.calls[-1][1]
     assert args[6] == t["page_table"].data_ptr() and args[7:10] == (3, 3, 16)
+
+
+def test_params_travel_after_a_call(recorded):
+    # what a call keeps with the parameter set stays behind
+    import copy
+    import pickle
+    p = csa.Params(topk=4, rope_factor=16.0, rope_orig_ctx=65536)
+    t = _keys(3, 3)
+    csa.csa_index_scores_mxfp4(p, *t.values(), torch.zeros(3, 1, 40))
+    L._ws_bytes(p, csa.CSA_OP_HCA_ATTN_PAGED, 1, 1, 64, -1)
+    for q in (copy.copy(p), copy.deepcopy(p), pickle.loads(pickle.dumps(p))):
+        assert q == p and hash(q) == hash(p)
+        csa.csa_index_scores_mxfp4(q, *t.values(), torch.zeros(3, 1, 40))
+        assert q.c() is not p.c() and bytes(q.c()) == bytes(p.c())
