@@ -215,7 +215,7 @@ def sparse_attn_paged(p: L.Params, q, q_pos, kv_pages, page_table, idx, kv_raw, 
     ws = ws or Workspace(q.device)
     B, Tq = q_pos.shape
     nb = L._ws_bytes(p, L.CSA_OP_SPARSE_ATTN_PAGED, B, Tq, page_table.shape[1] * kv_pages.shape[1],
-                     q.get_device())
+                     L._device_of(q, "q"))
     with _On(stream):
         if out is None:
             out = torch.empty_like(q)
@@ -232,7 +232,7 @@ def hca_decode_paged(p: L.Params, q, q_pos, kv_pages, page_table, n_cmp, kv_raw,
     ws = ws or Workspace(q.device)
     B, Tq = q_pos.shape
     nb = L._ws_bytes(p, L.CSA_OP_HCA_ATTN_PAGED, B, Tq, page_table.shape[1] * kv_pages.shape[1],
-                     q.get_device())
+                     L._device_of(q, "q"))
     with _On(stream):
         if out is None:
             out = torch.empty_like(q)
@@ -258,7 +258,7 @@ def csa_decode_paged(p: L.Params, q, q_pos, q_idx, w, k_codes, k_scales, n_cmp, 
     q_codes, q_scales = quantize_mxfp4(q_idx, stream)
     if n_max is None:
         n_max = page_table.shape[1] * k_codes.shape[1]
-    nb = L._ws_bytes(p, L.CSA_OP_INDEX_TOPK, B, Tq, n_max, q.get_device())
+    nb = L._ws_bytes(p, L.CSA_OP_INDEX_TOPK, B, Tq, n_max, L._device_of(q, "q"))
     with _On(stream):
         if idx is None:
             idx = torch.empty((B, Tq, p.topk), dtype=torch.int32, device=q.device)

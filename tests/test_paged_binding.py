@@ -73,3 +73,39 @@ def test_params_travel_after_a_call(recorded):
         assert q == p and hash(q) == hash(p)
         csa.csa_index_scores_mxfp4(q, *t.values(), torch.zeros(3, 1, 40))
         assert q.c() is not p.c() and bytes(q.c()) == bytes(p.c())
+
+
+class _OnDevice(torch.Tensor):
+    """A host tensor that says it is on cuda:1."""
+
+    def get_device(self):
+        return 1
+
+    @property
+    def device(self):
+        return torch.device("cuda", 1)
+
+
+@pytest.mark.parametrize("call", ["hca_decode_paged", "sparse_attn_paged", "csa_decode_paged"])
+def test_a_call_for_another_device_leaves_no_workspace_size(monkeypatch, call):
+    # sizes are asked of the current device; a tensor elsewhere is refused before
+    from sparse_compressed_attention_csa_b200 import layer
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    asked = []
+    monkeypatch.setattr(L, "csa_workspace_size", lambda *a: asked.append(a) or 256)
+    monkeypatch.setattr(layer, "quantize_mxfp4", lambda rows, stream=None: (rows, rows))
+    p = csa.Params(topk=4)
+    z = torch.zeros
+    q = z(2, 1, 128, 512).as_subclass(_OnDevice)
+    i1, i2, kv = z(2, dtype=I32), z(2, 1, dtype=I32), z(3, 16, 512)
+    tail = (z(2, 4, 512), i1, i1, z(128))
+    ws = layer.Workspace("cpu")
+    with pytest.raises(ValueError, match="current device is cuda:0"):
+        if call == "csa_decode_paged":
+            t = _keys(2, 2)
+            layer.csa_decode_paged(p, q, i2, z(2, 1, 64, 128), t["w"], t["k_codes"], t["k_scales"], i1, kv,
+                                   t["page_table"], *tail, ws=ws)
+        else:
+            sel = i1 if call == "hca_decode_paged" else z(2, 1, 4, dtype=I32)
+            getattr(layer, call)(p, q, i2, kv, z(2, 2, dtype=I32), sel, *tail, ws=ws)
+    assert not asked and not p.__dict__.get("_ws")
