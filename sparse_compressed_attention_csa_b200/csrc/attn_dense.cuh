@@ -355,7 +355,9 @@ __global__ void __launch_bounds__(kAdThreads, 1)
       const bool first = tb == 0, whole = first && te == x.tiles;
       // ---- RoPE table, then Q: the own dims to TMEM, the other dims in place
       asm volatile("bar.sync 1, 128;" ::: "memory");  // the last segment's table is done with
-      if (head < a.rope_dim / 2) {
+      // whole warps, also where rope_dim / 2 ends inside one (frequencies past
+      // it are 0): the barrier behind wants them converged
+      if (warp < kApMaxRope / 64) {
         float c, s;
         rope_cs_reduced(x.t, a.freq[head], &c, &s);
         sm.cs[head] = c;
@@ -933,7 +935,7 @@ __global__ void __launch_bounds__(kAdThreads, 1)
     const int piece = kApHeads * 4 * 32 * ((kApHalf / 32 + P - 1) / P);
     uint8_t* ml = ring + (P - 1) * piece + head * 8;  // + slot * 1 KB
     // a pair without tiles says so by l = -1
-    if (first == 0 && !have && head < a.rope_dim / 2)
+    if (warp < kApMaxRope / 64 && !have)
       rope_cs_reduced(a.q_pos[unit / a.groups], a.freq[head], &sm.cs[head], &sm.sn[head]);
     cluster_sync_all();  // the rings are free: every copy and product is done
     tc_fence_after();
