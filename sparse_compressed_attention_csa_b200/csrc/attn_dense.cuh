@@ -156,7 +156,7 @@ __device__ __forceinline__ AdUnit ad_unit(const AttnDenseArgs& a, int u) {
   x.n_sel = kSparse ? a.topk : max(0, min(n_visible(x.t, a.n_cmp[x.b], a.width, a.stride), a.n_max));
   const int rp0 = a.raw_pos0[x.b];
   const int lo = max(max(0, x.t - a.window + 1), rp0);
-  const int hi = min(x.t, rp0 + min(a.n_raw[x.b], a.raw_max) - 1);
+  const int hi = min(x.t, rp0 + (min(a.n_raw[x.b], a.raw_max) - 1));
   x.n_win = a.window > 0 && hi >= lo ? hi - lo + 1 : 0;
   x.raw_row = x.b * a.raw_max + (lo - rp0);
   x.win_tiles = (x.n_win + kAdTile - 1) / kAdTile;

@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(32 * kPgWarps) k_attn_paged_simt(const __grid_
   const int* sel = kHca ? nullptr : a.idx + (long long)token * a.topk;
   const int rp0 = a.raw_pos0[b];
   const int w_lo = max(max(0, t - a.window + 1), rp0);
-  const int w_hi = min(t, rp0 + min(a.n_raw[b], a.raw_max) - 1);
+  const int w_hi = min(t, rp0 + (min(a.n_raw[b], a.raw_max) - 1));
   const int n_win = a.window > 0 && w_hi >= w_lo ? w_hi - w_lo + 1 : 0;
   const long long n_rows = (long long)n_sel + n_win;
   const long long r0 = n_rows * split / a.splits, r1 = n_rows * (split + 1) / a.splits;

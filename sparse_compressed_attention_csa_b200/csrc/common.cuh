@@ -91,8 +91,8 @@ __device__ __forceinline__ void rope_cs_reduced(long long pos, double freq, floa
 // Entries j < n_cmp whose last pooled token s*j + w - 1 is at most t.
 __device__ __forceinline__ int n_visible(int t, int n_cmp, int width, int stride) {
   if (t < width - 1) return 0;
-  int v = (t - width + 1) / stride + 1;
-  return v < n_cmp ? v : n_cmp;
+  const int last = (t - width + 1) / stride;  // the last such entry (2^31 - 1 at most)
+  return last < n_cmp ? last + 1 : n_cmp;
 }
 
 // Order-preserving map fp32 -> uint32 (larger float, larger key); -0.0 is
