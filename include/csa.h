@@ -360,7 +360,8 @@ csa_status_t csa_quantize_mxfp4(csa_dtype_t dtype, const void* rows, int64_t row
  * the table entries of pages that hold a needed entry are read, and only the
  * needed rows count: the rest of a page may hold anything.  A table entry
  * outside [0, n_pages) records CSA_ERR_DEVICE_BOUNDS and its rows are
- * skipped.  Pages may be shared between sequences. */
+ * skipped.  Pages may be shared between sequences.  A table holds at most
+ * 2^31 - 2^15 rows a sequence (as n_max in every call), a pool 2^31 - 1. */
 
 /* Step 2a on MXFP4 queries and paged MXFP4 keys: csa_index_scores with
  *   q_codes [B][Tq][H_I][d_I / 2], q_scales [B][Tq][H_I][d_I / 32]

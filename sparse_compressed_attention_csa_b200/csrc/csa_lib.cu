@@ -193,7 +193,13 @@ csa_status_t check_dtype(csa_dtype_t dt) {
   return CSA_OK;
 }
 
+// Entries a call may be sized for: loops over entries step by up to 2^14 and
+// round up to that, all in 32 bits.
+constexpr int kMaxEntries = 0x7fffffff - (1 << 15) + 1;
+
 csa_status_t check_sizes(int B, int Tq, int n_max) {
+  if (n_max > kMaxEntries)
+    return fail(CSA_ERR_UNSUPPORTED_SHAPE, "%d entries: at most %d (2^31 - 2^15)", n_max, kMaxEntries);
   // query rows (B * Tq) index a grid dimension of at most 65535 blocks
   if (B < 1 || Tq < 1 || n_max < 0 || (long long)B * Tq > 65535)
     return fail(CSA_ERR_UNSUPPORTED_SHAPE, "B=%d Tq=%d n_max=%d out of range (B*Tq <= 65535)",
