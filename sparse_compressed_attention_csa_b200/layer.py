@@ -20,19 +20,60 @@ import torch
 from . import _lib as L
 
 
+class _On:
+    """What a call allocates is allocated for the stream it runs on (torch's
+    allocator hands a freed block to the stream it came from)."""
+
+    def __init__(self, stream):
+        self.ctx = None if stream is None else torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
 class Workspace:
-    """A reusable device scratch buffer that grows on demand."""
+    """A reusable device scratch buffer that grows on demand.  Calls that share
+    one run one after another (on one stream, or ordered by events; replays of
+    graphs that were captured with it included).  A buffer that a captured graph
+    uses stays until the workspace is dropped, and an outgrown one is not handed
+    out again before the calls on it are over, on whichever stream they run."""
 
     def __init__(self, device=None):
         self.device = device
         self.buf = None
+        self._in_graph = False  # a capture has used `buf`
+        self._kept = []         # outgrown buffers of captured graphs
 
     def get(self, nbytes: int):
+        """At least `nbytes`, for calls on the current stream."""
         if nbytes == 0:
             return None
         if self.buf is None or self.buf.numel() < nbytes:
+            if self._in_graph:
+                self._kept.append(self.buf)
+                self._in_graph = False
             self.buf = torch.empty(nbytes, dtype=torch.uint8, device=self.device or "cuda")
+            self._home = self._current()
+        if self.buf.is_cuda:
+            if torch.cuda.is_current_stream_capturing():
+                self._in_graph = True
+            elif self._current() != self._home:
+                self.buf.record_stream(torch.cuda.current_stream(self.buf.device))
         return self.buf
+
+    def on(self, nbytes: int, stream):
+        """get() for a call on `stream` (None: the current one)."""
+        with _On(stream):
+            return self.get(nbytes)
+
+    def _current(self):
+        """The current stream's handle."""
+        return torch._C._cuda_getCurrentRawStream(self.buf.device.index) if self.buf.is_cuda else 0
 
 
 def csa_decode(p: L.Params, q, q_pos, q_idx, w, k_idx, n_cmp, kv_cmp, kv_raw, raw_pos0, n_raw,
@@ -46,9 +87,9 @@ def csa_decode(p: L.Params, q, q_pos, q_idx, w, k_idx, n_cmp, kv_cmp, kv_raw, ra
     if out is None:
         out = torch.empty_like(q)
     nb = L.csa_workspace_size(p, L.CSA_OP_INDEX_TOPK, B, Tq, n_max)
-    L.csa_index_topk(p, q_idx, w, k_idx, q_pos, n_cmp, idx, ws.get(nb), stream)
+    L.csa_index_topk(p, q_idx, w, k_idx, q_pos, n_cmp, idx, ws.on(nb, stream), stream)
     nb = L.csa_workspace_size(p, L.CSA_OP_SPARSE_ATTN, B, Tq, kv_cmp.shape[1])
-    L.csa_sparse_attn(p, q, q_pos, kv_cmp, idx, kv_raw, raw_pos0, n_raw, sink, out, ws.get(nb),
+    L.csa_sparse_attn(p, q, q_pos, kv_cmp, idx, kv_raw, raw_pos0, n_raw, sink, out, ws.on(nb, stream),
                       stream)
     return idx, out
 
@@ -79,7 +120,7 @@ def hca_decode(p: L.Params, q, q_pos, kv_cmp, n_cmp, kv_raw, raw_pos0, n_raw, si
     if out is None:
         out = torch.empty_like(q)
     nb = L.csa_workspace_size(p, L.CSA_OP_HCA_ATTN, B, Tq, kv_cmp.shape[1])
-    L.hca_attn(p, q, q_pos, kv_cmp, n_cmp, kv_raw, raw_pos0, n_raw, sink, out, ws.get(nb), stream)
+    L.hca_attn(p, q, q_pos, kv_cmp, n_cmp, kv_raw, raw_pos0, n_raw, sink, out, ws.on(nb, stream), stream)
     return out
 
 
@@ -101,7 +142,7 @@ def reuse_attn(p: L.Params, q, q_pos, kv_cmp, idx, kv_raw, raw_pos0, n_raw, sink
     R = q.shape[0]
     B, Tq = q_pos.shape
     nb = L.csa_workspace_size(p, L.CSA_OP_SPARSE_ATTN, R * B, Tq, kv_cmp.shape[1])
-    L.csa_reuse_attn(p, q, q_pos, kv_cmp, idx, kv_raw, raw_pos0, n_raw, sink, out, ws.get(nb),
+    L.csa_reuse_attn(p, q, q_pos, kv_cmp, idx, kv_raw, raw_pos0, n_raw, sink, out, ws.on(nb, stream),
                      stream)
     return out[0] if single else out
 
@@ -158,27 +199,11 @@ def csa_decode_fp8(p: L.Params, q, q_pos, q_idx, w, k_idx, n_cmp, kv_cmp, cmp_sc
     if out is None:
         out = torch.empty_like(q)
     nb = L.csa_workspace_size(p, L.CSA_OP_INDEX_TOPK, B, Tq, n_max)
-    L.csa_index_topk(p, q_idx, w, k_idx, q_pos, n_cmp, idx, ws.get(nb), stream)
+    L.csa_index_topk(p, q_idx, w, k_idx, q_pos, n_cmp, idx, ws.on(nb, stream), stream)
     nb = L.csa_workspace_size(p, L.CSA_OP_SPARSE_ATTN, B, Tq, kv_cmp.shape[1])
     L.csa_sparse_attn_fp8(p, q, q_pos, kv_cmp, cmp_scale, idx, kv_raw, raw_scale, raw_pos0, n_raw,
-                          sink, out, ws.get(nb), stream)
+                          sink, out, ws.on(nb, stream), stream)
     return idx, out
-
-
-class _On:
-    """What a call allocates is allocated for the stream it runs on (torch's
-    allocator hands a freed block to the stream it came from)."""
-
-    def __init__(self, stream):
-        self.ctx = None if stream is None else torch.cuda.stream(stream)
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
 
 
 def norm_rope(p: L.Params, q, q_weight=None, q_pos=None, k=None, k_weight=None, k_pos=None,
