@@ -58,16 +58,19 @@ class Workspace:
                 self._kept.append(self.buf)
                 self._in_graph = False
             self.buf = torch.empty(nbytes, dtype=torch.uint8, device=self.device or "cuda")
-            self._home = self._current()
+            self._streams = {self._current()}
         if self.buf.is_cuda:
             if torch.cuda.is_current_stream_capturing():
                 self._in_graph = True
-            elif self._current() != self._home:
+            elif self._current() not in self._streams:  # once: it counts until the buffer is freed
                 self.buf.record_stream(torch.cuda.current_stream(self.buf.device))
+                self._streams.add(self._current())
         return self.buf
 
     def on(self, nbytes: int, stream):
         """get() for a call on `stream` (None: the current one)."""
+        if stream is None:
+            return self.get(nbytes)
         with _On(stream):
             return self.get(nbytes)
 
