@@ -310,7 +310,9 @@ csa_status_t hca_attn_fp8(const csa_params_t* p, const void* q, const int32_t* q
  * then the trailing p->rope_dim dims of y are rotated by pos[r] (interleaved
  * pairs, p's frequencies, YaRN included), both in fp32 with one rounding to
  * the dtype.  It prepares the indexer's queries and keys, and token rows or
- * pooled entries for a paged cache.
+ * pooled entries for a paged cache (entries that are not rotated yet:
+ * csa_compress or csa_compress_append with rope_dim = 0 gives them, and k_pos is
+ * then stride * j + pos_offset).
  *   q  [q_rows][q_heads][dim], row r at q + r * q_stride elements (q_stride
  *      >= q_heads * dim, q_stride * element size a multiple of 16); q_out
  *      [q_rows][q_heads][dim] dense

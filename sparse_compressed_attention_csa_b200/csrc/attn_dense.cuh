@@ -21,9 +21,18 @@
 // here, more than the second S.  What bounds it: per 64 rows a CTA has 1,790
 // clocks of MMAs (16 x 48 with A in shared memory, 16 x 32 with A in TMEM, N =
 // 64; 4 x 128, N = 256) and 224 KB through shared memory (1,750 clocks); it
-// takes about 2,500.  8 ragged sequences of up to 64K rows: 91 us; 16 x 1,152
-// rows: 21.2 us; 32 x 1,152 selected rows: 26.6 us (42 on k_attn_pair with paged
-// rows): about 4 us before the first MMA, 1.35 a tile, 5 to join the parts.
+// takes about 2,500.  8 ragged sequences of up to 64K rows (230 MB): 97 to 102 us
+// over inputs that the L2 does not hold (116 on one box), 91 replayed on one set
+// of them; 16 x 1,152 rows: 21.2 us; 32 x 1,152 selected rows: 26.6 us (42 on
+// k_attn_pair with paged rows): about 4 us before the first MMA, 1.35 a tile, 5
+// to join the parts.  Chunks of a prompt: 1,024 tokens x 1,152 selected rows 0.46
+// to 0.52 ms (618 TFLOP/s), 512 tokens x 16,384 rows 2.4 to 2.9 ms (780 TFLOP/s);
+// a pair takes 9 to 14 us to go from a token to the next (Q in, O out).
+// Fewer heads cost the same: M is 128 whatever the group holds (16 heads: 16 x
+// 1,152 rows 23 to 25 us).
+//
+// Rotated Q is rounded to bf16, as the operand of the product (half a step is
+// 2^-8 of each value, what Q came with).
 //
 // TMEM (512 columns): O [0,256) | S [256,384) two buffers | Q of the own dims
 // as bf16 pairs [384,512).  Q of the other dims stays in shared memory (64
@@ -81,7 +90,7 @@ constexpr int kAdThreads = 320;
 // 94.6 us, 2 tiles 91.4, 4 tiles 92.3, 6 tiles 92.9)
 constexpr int kAdAhead = 2;
 constexpr int kAdMasks = 8;            // more tiles than the ring lets the fetch run ahead
-constexpr int kAdSegTiles = 3;         // what changing tokens costs a pair, in tiles
+constexpr int kAdSegTiles = 3;         // tiles above the mean at which equal ranges take over
 constexpr int kAdFixedTiles = 6;       // what the device's ranges and the join cost, in tiles
 constexpr int kAdMaxPairs = 128;       // units a one-token-per-pair plan may hold
 constexpr size_t kAdPartHalfs = 2 * (size_t)kApHeads * kApHalf;  // fp16 values of one part
@@ -512,8 +521,8 @@ __global__ void __launch_bounds__(kAdThreads, 1)
         const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
-          // the sum in fp32; P in bf16, the operand of the product (2^-9 of
-          // each weight, where the output keeps as many bits)
+          // the sum in fp32; P in bf16, the operand of the product (half a step
+          // is 2^-8 of each weight; the output keeps as many bits)
           const float p0 = ap_ex2(fmaf(z[2 * e], a.scale_log2, neg_m));
           const float p1 = ap_ex2(fmaf(z[2 * e + 1], a.scale_log2, neg_m));
           ps8[e & 7] += p0 + p1;

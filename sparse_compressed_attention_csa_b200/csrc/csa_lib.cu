@@ -554,7 +554,9 @@ int attn_dense_clusters(int pairs) {
 // kernel): the most that fit the GPU at once, as long as the longest unit takes
 // no more than kAdFixedTiles tiles per pair above an even share.  Entries to
 // attend are topk for every selecting token; of a dense cache the host knows
-// only the most, so an even share counts as nothing there.
+// only the most that the page table holds, so an even share counts as nothing
+// there, and a table much wider than its sequences are long takes the ranges (16
+// x 1,152 rows: 21.2 us in clusters, 23.1 in ranges).
 template <bool kSparse>
 int attn_dense_fixed(long long units, long long tiles, int pairs) {
   const long long even = kSparse ? (units * tiles + pairs - 1) / pairs : 0;

@@ -32,10 +32,12 @@
 // prefill), CTAs take whole units in turn, back and forth, the last (the
 // longest under a causal mask) first.
 //
-// Measured: 32 x 16,383 keys (38 MB) 14.8 us a call, 2.6 TB/s; the plan, the
-// first tile's trip to memory and the last tile's epilogue are about half of
-// it.  8,192 causal tokens 101 us, 1.36 PFLOP/s; issue slots 56% busy, the
-// accumulators' hand-over between MMA and epilogue is the rest.
+// Measured: 32 x 16,383 keys (38 MB) 14.8 us a call, 2.6 TB/s, over three sets of
+// inputs that the L2 nearly holds (18.5 us alone and cold; the bf16 indexer on
+// contiguous keys 27 us in the same loop); the plan, the first tile's trip to
+// memory and the last tile's epilogue are about half of it.  8,192 causal tokens
+// 103 us, 1.33 PFLOP/s; issue slots 56% busy, the accumulators' hand-over between
+// MMA and epilogue is the rest.
 #pragma once
 #include <type_traits>
 

@@ -14,12 +14,15 @@
 // bits rounds to code 0 either way), so the codes depend on no rounding but
 // their own.
 //
-// Quantizer: HBM-bound.  A lane takes 8 values (16 bytes of bf16, 32 of
-// fp32), four neighbouring lanes a block: two shuffles give the block's
-// maximum, one conversion instruction packs each pair of values.  524,256 keys
-// of 128 in bf16 into random rows, values written too: 63 us, 4.8 TB/s, 74% of
-// the copy rate; two such pieces per thread (66.5 us with one, 78 with four).
-// The rest is the 4-byte scale rows, each a part of a 32-byte sector.
+// Quantizer.  A lane takes 8 values (16 bytes of bf16, 32 of fp32), four
+// neighbouring lanes a block: two shuffles give the block's maximum, one
+// conversion instruction packs each pair of values.  524,256 keys of 128 into
+// random rows, values written too: fp32 94 us, 6.1 TB/s, 93% of the copy rate
+// (HBM-bound); bf16 63 us, 4.8 TB/s, 74%, with 72% of the issue slots busy: the
+// same instructions over half the bytes.  Two such pieces per thread (bf16:
+// 66.5 us with one, 78 with four).  The 4-byte scale rows, each a part of a
+// 32-byte sector, do not show: fp32 writes the same ones, and nothing is read
+// to fill sectors (136 MB read where rows and slots are 136).
 #pragma once
 #include "common.cuh"
 #include "quantize.cuh"
@@ -204,7 +207,9 @@ struct PageWindow {
 
 // Indexer scores on CUDA cores, any head count and dim: one key per thread,
 // the query's dequantized heads and weights in shared memory, 16 heads at a
-// time, 32 dims (one scale) of the key in registers.
+// time, 32 dims (one scale) of the key in registers.  Bound by its multiply-adds
+// and their reads of shared memory: 32 x 16,383 keys under 32 heads of 128, or 64
+// of 64, 240 us (18 TFLOP/s).
 __global__ void __launch_bounds__(128)
     k_index_scores_mx_simt(const uint8_t* __restrict__ q_codes, const uint8_t* __restrict__ q_scales,
                            const float* __restrict__ w, const uint8_t* __restrict__ k_codes,

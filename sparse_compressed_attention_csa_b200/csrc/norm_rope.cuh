@@ -16,11 +16,13 @@
 //
 // Heads per group: 1 while the rows are few (a decode step's 2,048 heads of
 // 128: 4.2 us, a launch and one trip to memory), up to 32 while the groups
-// still fill the GPU 16 times: 8,192 tokens x 128 heads of 512 in bf16 take 373
-// us, 5.8 TB/s, 89% of the copy rate (432 us with 8 heads a group, 392 with 16;
-// the sines are then formed for fewer groups).  Two heads a turn keep two rows
-// in flight and overlap their shuffles: 890 -> 426 us together with holding the
-// next rows as loaded (16 bytes) instead of converted.
+// still fill the GPU 16 times: 8,192 tokens x 128 heads of 512 in bf16 take 377
+// us, 5.7 TB/s, 87% of the copy rate (388 on one box; 432 us with 8 heads a
+// group, 392 with 16; the sines are then formed for fewer groups), 8,192 x 128
+// heads of 128 in fp32 176 us (94%), 8,192 x 32 of 512 in fp32, one head at a
+// time, 193 us (88%).  Two heads a turn keep two rows in flight and overlap
+// their shuffles: 890 -> 426 us together with holding the next rows as loaded
+// (16 bytes) instead of converted.
 #pragma once
 #include "common.cuh"
 #include "compress.cuh"
